@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhstu.so")
 SOURCES = ["hstu_api.cu"]
 HEADERS = ["ptx.cuh", "status.cuh", "attn.cuh", "attn_bwd.cuh", "gemm.cuh", "fp32_path.cuh",
-           "sl.cuh", "layer_bwd.cuh"]
+           "sl.cuh", "layer_bwd.cuh", "cache.cuh", "paged_attn.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -17,9 +17,11 @@
 #include "../../include/hstu.h"
 #include "attn.cuh"
 #include "attn_bwd.cuh"
+#include "cache.cuh"
 #include "fp32_path.cuh"
 #include "gemm.cuh"
 #include "layer_bwd.cuh"
+#include "paged_attn.cuh"
 #include "sl.cuh"
 
 using namespace hstu;
@@ -106,14 +108,15 @@ const int64_t* thresholds_for(int Tb) {
 enum KernelKind : int {
   K_F1 = 0, K_ATTN, K_F2, K_CAND_ATTN, K_SCORE, K_F32_LINEAR, K_F32_ATTN, K_F32_LN, K_CVT,
   K_SL, K_SL_GATHER, K_ATTN_FUSED, K_ATTN_BWD, K_BWD_GEMM, K_GATE_BWD,
-  K_BWD_ELT, K_COUNT
+  K_BWD_ELT, K_CACHE_META, K_CACHE_ROWS, K_PAGED_ATTN, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {"f1_gemm",     "attention",      "f2_gemm",
                                            "mfalcon_attention", "score",    "fp32_linear",
                                            "fp32_attention",    "fp32_ln_gate", "weight_cvt",
                                            "sl_select",         "sl_gather",
                                            "attention_f2_fused", "attention_bwd",
-                                           "bwd_gemm_cublas", "gate_bwd", "bwd_elementwise"};
+                                           "bwd_gemm_cublas", "gate_bwd", "bwd_elementwise",
+                                           "cache_pages", "cache_rows", "paged_attention"};
 
 struct Profiler {
   std::mutex mu;
@@ -212,6 +215,23 @@ AttnBwdFn attn_bwd_kernel_ptr(int phi, bool f16) {
   return f16 ? attn_bwd_kernel_for<true>(phi) : attn_bwd_kernel_for<false>(phi);
 }
 
+using PagedRowsFn = void (*)(const CUtensorMap, const PagedParams);
+
+template <bool F16, int MT>
+PagedRowsFn paged_rows_kernel_for(int phi) {
+  switch (phi) {
+    case HSTU_ACT_SILU: return hstu_paged_rows_kernel<HSTU_ACT_SILU, F16, MT>;
+    case HSTU_ACT_RELU: return hstu_paged_rows_kernel<HSTU_ACT_RELU, F16, MT>;
+    case HSTU_ACT_SOFTMAX: return hstu_paged_rows_kernel<HSTU_ACT_SOFTMAX, F16, MT>;
+    default: return hstu_paged_rows_kernel<HSTU_ACT_IDENTITY, F16, MT>;
+  }
+}
+
+PagedRowsFn paged_rows_kernel_ptr(int phi, bool f16, int mt) {
+  if (f16) return mt == 1 ? paged_rows_kernel_for<true, 1>(phi) : paged_rows_kernel_for<true, 2>(phi);
+  return mt == 1 ? paged_rows_kernel_for<false, 1>(phi) : paged_rows_kernel_for<false, 2>(phi);
+}
+
 struct DeviceInfo {
   int sm_count = 0;
   bool smem_set = false;
@@ -245,6 +265,12 @@ hstu_status_t device_info(DeviceInfo** out) {
       for (int f16 = 0; f16 < 2; ++f16)
         HSTU_CHECK_CUDA(cudaFuncSetAttribute(attn_bwd_kernel_ptr(phi, f16 != 0),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, att_max));
+    for (int phi = 0; phi < 4; ++phi)
+      for (int f16 = 0; f16 < 2; ++f16)
+        for (int mt = 1; mt <= 2; ++mt)
+          HSTU_CHECK_CUDA(cudaFuncSetAttribute(paged_rows_kernel_ptr(phi, f16 != 0, mt),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(PgsSmem::kBytes)));
     const int g1 = static_cast<int>(F1Smem::kBytes);
     HSTU_CHECK_CUDA(cudaFuncSetAttribute(hstu_f1_kernel<HSTU_ACT_RELU>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, g1));
@@ -495,6 +521,10 @@ struct AttnJob {
   float* ln_part;
   uint64_t timeout_ns;
   bool f16;                     // Q, K, V (and P) in fp16 instead of bf16
+  // new events over the paged cache: the layer appends its K and V there and
+  // attends to the sequences' pages
+  const struct PagedJob* paged;
+  int32_t paged_layer;
   // layer-fused f2 (causal, f16): tail.count is [T_q] and zeroed here; w2h is
   // the fp16 W2 [d, H*64]
   const TailParams* tail = nullptr;
@@ -833,6 +863,236 @@ hstu_status_t launch_f32_attn(const AttnJob& j, cudaStream_t st) {
   return HSTU_OK;
 }
 
+// ------------------------------------------------------------------ paged cache
+
+size_t cache_elt(const hstu_cache_t* c) { return c->dtype == HSTU_FP32 ? 4 : 2; }
+
+int log2_of(int v) {
+  int k = 0;
+  while ((1 << k) < v) ++k;
+  return k;
+}
+
+// `refs`: the call reads or writes ref_count.
+hstu_status_t check_cache(const hstu_cache_t* c, bool refs) {
+  if (c == nullptr || c->num_layers < 1 || c->num_heads < 1 || c->num_pages < 1 || c->num_seqs < 1 ||
+      c->max_blocks < 1)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (c->dtype != HSTU_BF16 && c->dtype != HSTU_FP32 && c->dtype != HSTU_FP16)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (c->kv == nullptr || c->timestamps == nullptr || c->block_table == nullptr ||
+      c->lengths == nullptr || (refs && c->ref_count == nullptr))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (!aligned16(c->kv)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return HSTU_ERR_UNSUPPORTED;
+  // one layer's page rows are a tensor-map coordinate; positions are int32
+  const int64_t limit = (int64_t(1) << 31) - 64;
+  if (static_cast<int64_t>(c->num_heads) * ATT_HD > 8192 || c->num_layers > 65534)
+    return HSTU_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->num_pages) * 2 * c->num_heads * c->page_size >= limit ||
+      c->max_blocks > (1 << 20) || static_cast<int64_t>(c->max_blocks) * c->page_size >= limit)
+    return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+// The jagged description of new events: no length limit but the sequence's own,
+// timestamps where rows exist.
+hstu_status_t check_chunk(const hstu_jagged_t* j) {
+  if (j == nullptr || j->batch < 0 || j->total_tokens < 0 || j->max_len < 0)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (j->batch > 0 && j->offsets == nullptr) return HSTU_ERR_INVALID_ARGUMENT;
+  if (j->total_tokens > 0 && (j->timestamps == nullptr || j->batch == 0 || j->max_len == 0))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (j->segments != nullptr) return HSTU_ERR_UNSUPPORTED;
+  if (j->batch > 65535 || j->total_tokens > (int64_t(1) << 31) - 1) return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+CacheView view_of(const hstu_cache_t* c) {
+  CacheView v;
+  v.kv = static_cast<uint8_t*>(c->kv);
+  v.ts = c->timestamps;
+  v.ref = c->ref_count;
+  v.table = c->block_table;
+  v.lengths = c->lengths;
+  v.L = c->num_layers;
+  v.num_pages = c->num_pages;
+  v.H = c->num_heads;
+  v.ps_log2 = log2_of(c->page_size);
+  v.max_blocks = c->max_blocks;
+  v.num_seqs = c->num_seqs;
+  v.elt = static_cast<int32_t>(cache_elt(c));
+  return v;
+}
+
+// Workspace of the bookkeeping: [state / count][B: old length, first, (src, dst)]
+// [num_pages ids] for reserve, [count][3 x num_pages] for compact.
+size_t cache_ws_bytes(const hstu_cache_t* c, int32_t batch) {
+  const size_t pages = align_up(static_cast<size_t>(c->num_pages) * 4, 256);
+  const size_t b = align_up(static_cast<size_t>(batch) * 16, 256);
+  return 256 + std::max(b + pages, 3 * pages);
+}
+
+ReserveWs carve_reserve(const hstu_cache_t*, int32_t batch, void* ws) {
+  ReserveWs r;
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  r.state = reinterpret_cast<int32_t*>(p);
+  int32_t* b = reinterpret_cast<int32_t*>(p + 256);
+  r.old_len = b;
+  r.first = b + batch;
+  r.cow = b + 2 * static_cast<size_t>(batch);
+  r.pages = reinterpret_cast<int32_t*>(p + 256 + align_up(static_cast<size_t>(batch) * 16, 256));
+  return r;
+}
+
+hstu_status_t launch_reserve(const hstu_cache_t* c, const hstu_jagged_t* chunk, const int32_t* seq_ids,
+                             const ReserveWs& ws, cudaStream_t st) {
+  const CacheView v = view_of(c);
+  ProfScope prof(K_CACHE_META, st);
+  hstu_cache_reserve_kernel<<<1, CACHE_META_THREADS, 0, st>>>(v, chunk->batch, seq_ids, chunk->offsets,
+                                                              chunk->total_tokens, chunk->max_len, ws);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  const dim3 grid(chunk->batch, c->num_layers + 1);
+  hstu_cache_reserve_rows_kernel<<<grid, CACHE_COPY_THREADS, 0, st>>>(v, seq_ids, chunk->offsets,
+                                                                     chunk->timestamps, ws);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+// Row movers: blocks of 8 warps, about 8 blocks per SM over all users, at most
+// what the longest user needs.
+unsigned mover_blocks(int sm_count, int64_t max_rows, int64_t users) {
+  const int64_t want = (max_rows + 7) / 8;
+  const int64_t fair = std::max<int64_t>(1, static_cast<int64_t>(sm_count) * 8 / std::max<int64_t>(users, 1));
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min(want, fair)));
+}
+
+hstu_status_t launch_append(const hstu_cache_t* c, int layer, const hstu_jagged_t* chunk,
+                            const int32_t* seq_ids, const void* k, int64_t ldk, const void* v,
+                            int64_t ldv, const int32_t* go, cudaStream_t st) {
+  DeviceInfo* di = nullptr;
+  hstu_status_t s = device_info(&di);
+  if (s != HSTU_OK) return s;
+  const dim3 grid(mover_blocks(di->sm_count, chunk->max_len, chunk->batch), chunk->batch);
+  ProfScope prof(K_CACHE_ROWS, st);
+  hstu_cache_append_kernel<<<grid, CACHE_COPY_THREADS, 0, st>>>(
+      view_of(c), layer, seq_ids, chunk->offsets, chunk->total_tokens, chunk->max_len,
+      static_cast<const uint8_t*>(k), ldk, static_cast<const uint8_t*>(v), ldv, go);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+struct PagedJob {
+  const hstu_cache_t* cache;
+  const hstu_jagged_t* chunk;
+  const int32_t* seq_ids;
+  int32_t max_context, window, sinks;
+  const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
+};
+
+// Largest power of two of CTAs per cluster (at most 8, the portable size) that
+// still leaves every CTA `min_tiles` key tiles of the longest context, taken only
+// as far as the grid needs it to reach `want` CTAs.
+int paged_splits(int64_t ctas, int64_t want, int max_tiles, int min_tiles) {
+  int ns = 1;
+  while (ns < 8 && ctas * ns < want && max_tiles >= 2 * ns * min_tiles) ns *= 2;
+  return ns;
+}
+
+template <class Fn, class... Args>
+hstu_status_t launch_cluster(Fn fn, int64_t ctas, int ns, int threads, size_t smem, cudaStream_t st,
+                             Args... args) {
+  if (ctas * ns > (int64_t(1) << 31) - 1) return HSTU_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t lc;
+  std::memset(&lc, 0, sizeof(lc));
+  lc.gridDim = dim3(static_cast<unsigned>(ctas * ns));
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ns;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  HSTU_CHECK_CUDA(cudaLaunchKernelEx(&lc, fn, args...));
+  return HSTU_OK;
+}
+
+// av: operand type; av_f32 (and ln_part) instead of it when given.
+hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, int layer, const void* q,
+                                int64_t ldq, const float* rab_pos, const float* rab_time, void* av,
+                                float* av_f32, float* ln_part, cudaStream_t st) {
+  if (j.chunk->batch == 0 || j.chunk->total_tokens == 0) return HSTU_OK;
+  DeviceInfo* di = nullptr;
+  hstu_status_t s = device_info(&di);
+  if (s != HSTU_OK) return s;
+  const hstu_cache_t* ca = j.cache;
+  PagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  const size_t layer_bytes =
+      static_cast<size_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size * 64 * cache_elt(ca);
+  p.kv = static_cast<const uint8_t*>(ca->kv) + layer_bytes * layer;
+  p.ts = ca->timestamps;
+  p.table = ca->block_table;
+  p.lengths = ca->lengths;
+  p.seq_ids = j.seq_ids;
+  p.q_offsets = j.chunk->offsets;
+  p.q_ts = j.chunk->timestamps;
+  p.q = q;
+  p.ldq = ldq;
+  p.rab_pos = rab_pos;
+  p.rab_time = rab_time;
+  p.av = av;
+  p.av_f32 = av_f32;
+  p.ln_part = ln_part;
+  p.T = j.chunk->total_tokens;
+  p.B = j.chunk->batch;
+  p.H = c->num_heads;
+  p.P = c->num_pos_buckets;
+  p.Tb = c->num_time_buckets;
+  p.num_pages = ca->num_pages;
+  p.num_seqs = ca->num_seqs;
+  p.max_blocks = ca->max_blocks;
+  p.ps_log2 = log2_of(ca->page_size);
+  p.max_new = j.chunk->max_len;
+  p.max_context = static_cast<int32_t>(
+      std::min<int64_t>(j.max_context, static_cast<int64_t>(ca->max_blocks) * ca->page_size));
+  p.window = j.window;
+  p.sinks = j.window > 0 ? j.sinks : 0;
+  p.timeout_ns = kDefaultTimeoutNs;
+  const int64_t* thr = thresholds_for(c->num_time_buckets);
+  for (int b = 0; b < c->num_time_buckets; ++b)
+    p.thr[b] = thr[b] < static_cast<int64_t>(INT32_MAX) ? static_cast<int32_t>(thr[b]) : INT32_MAX;
+  if (!compute_octaves(c->num_time_buckets, thr, p.oct)) return HSTU_ERR_UNSUPPORTED;
+  const int max_new = std::min(p.max_new, p.max_context);
+  if (max_new == 0) return HSTU_OK;
+  // the longest visible part of a context, in key tiles
+  int64_t seen = p.max_context;
+  if (p.window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(p.window) + max_new + p.sinks);
+  const int max_tiles = static_cast<int>((seen + PG_KEYS - 1) / PG_KEYS);
+  ProfScope prof(K_PAGED_ATTN, st);
+  if (ca->dtype == HSTU_FP32) {
+    p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
+    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
+    p.nsplit = paged_splits(ctas, 2 * di->sm_count, max_tiles, 1);
+    return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
+  }
+  const bool f16 = ca->dtype == HSTU_FP16;
+  CUtensorMap mkv;
+  const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
+  if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, PG_KEYS), f16)) != HSTU_OK)
+    return s;
+  const int mt = max_new <= 16 ? 1 : 2;
+  p.groups = (max_new + 16 * mt - 1) / (16 * mt);
+  const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
+  p.nsplit = paged_splits(ctas, 4 * di->sm_count, max_tiles, 2);
+  return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mt), ctas, p.nsplit, PGS_THREADS,
+                        PgsSmem::kBytes, st, mkv, p);
+}
+
 // One layer on the fp32 path.
 hstu_status_t layer_fp32(const hstu_layer_cfg_t* c, const hstu_layer_weights_t* w,
                          const AttnJob& base, const float* x_in, const float* x_res, int64_t T,
@@ -863,7 +1123,17 @@ hstu_status_t layer_fp32(const hstu_layer_cfg_t* c, const hstu_layer_weights_t* 
   j.rab_time = w->rab_time;
   j.av = ws.av;
   j.ld_av = hv;
-  if ((s = launch_f32_attn(j, st)) != HSTU_OK) return s;
+  if (j.paged != nullptr) {
+    const PagedJob& pj = *j.paged;
+    if ((s = launch_append(pj.cache, j.paged_layer, pj.chunk, pj.seq_ids, dst[3], n1, dst[1], n1, pj.go,
+                           st)) != HSTU_OK)
+      return s;
+    s = launch_paged_attn(c, pj, j.paged_layer, dst[2], n1, w->rab_pos, w->rab_time, nullptr,
+                          static_cast<float*>(ws.av), nullptr, st);
+  } else {
+    s = launch_f32_attn(j, st);
+  }
+  if (s != HSTU_OK) return s;
   float* g = static_cast<float*>(ws.extra);
   const unsigned blocks = static_cast<unsigned>((T * 32 + 255) / 256);
   ProfScope prof(K_F32_LN, st);
@@ -930,8 +1200,8 @@ hstu_status_t layer_bf16(const hstu_layer_cfg_t* c, const hstu_layer_weights_t* 
   j.f16 = true;
   // on request, causal layers with d <= 512 and H * 64 <= 512 run f2 inside
   // the attention kernel (the tail of the last head CTA of each query tile pair)
-  const bool fused = !cand && (c->flags & HSTU_FLAG_FUSED_F2) != 0 && c->d_model <= 512 &&
-                     hv <= 512;
+  const bool fused = !cand && j.paged == nullptr && (c->flags & HSTU_FLAG_FUSED_F2) != 0 &&
+                     c->d_model <= 512 && hv <= 512;
   if (fused) {
     TailParams tp;
     std::memset(&tp, 0, sizeof(tp));
@@ -955,7 +1225,16 @@ hstu_status_t layer_bf16(const hstu_layer_cfg_t* c, const hstu_layer_weights_t* 
     j.w2h = ws.w2h;
     return launch_attn_tc<false>(j, st);
   }
-  s = cand ? launch_attn_tc<true>(j, st) : launch_attn_tc<false>(j, st);
+  if (j.paged != nullptr) {
+    const PagedJob& pj = *j.paged;
+    if ((s = launch_append(pj.cache, j.paged_layer, pj.chunk, pj.seq_ids, dst[3], ldd[3], dst[1], ldd[1],
+                           pj.go, st)) != HSTU_OK)
+      return s;
+    s = launch_paged_attn(c, pj, j.paged_layer, dst[2], ldd[2], w->rab_pos, w->rab_time, nullptr,
+                          j.av_f32, j.ln_part, st);
+  } else {
+    s = cand ? launch_attn_tc<true>(j, st) : launch_attn_tc<false>(j, st);
+  }
   if (s != HSTU_OK) return s;
   return launch_f2_bf16(c, w, ws.w2h, true, static_cast<const float*>(ws.av), hv, ws.u, hv,
                         static_cast<const float*>(ws.extra), x_res, x_in, d, y_out, y_lp,
@@ -1676,6 +1955,239 @@ hstu_status_t mfalcon_score(const hstu_layer_cfg_t* cfg, int32_t num_layers,
     hstu_score_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(
         yfin, d, static_cast<const __nv_bfloat16*>(cand_emb), d, M, d, scores);
   HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+size_t hstu_cache_workspace_bytes(const hstu_cache_t* cache, int32_t batch) {
+  if (check_cache(cache, false) != HSTU_OK || batch < 0) return 0;
+  return cache_ws_bytes(cache, batch);
+}
+
+hstu_status_t hstu_cache_reserve(const hstu_cache_t* cache, const hstu_jagged_t* chunk,
+                                 const int32_t* seq_ids, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, true)) != HSTU_OK) return s;
+  if ((s = check_chunk(chunk)) != HSTU_OK) return s;
+  if (chunk->batch == 0) return HSTU_OK;
+  if (!aligned16(workspace)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (workspace == nullptr || ws_bytes < cache_ws_bytes(cache, chunk->batch))
+    return HSTU_ERR_WORKSPACE_TOO_SMALL;
+  return launch_reserve(cache, chunk, seq_ids, carve_reserve(cache, chunk->batch, workspace),
+                        static_cast<cudaStream_t>(stream));
+}
+
+hstu_status_t hstu_cache_append(const hstu_cache_t* cache, int32_t layer,
+                                const hstu_jagged_t* chunk, const int32_t* seq_ids, const void* k,
+                                int64_t ldk, const void* v, int64_t ldv, void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, false)) != HSTU_OK) return s;
+  if ((s = check_chunk(chunk)) != HSTU_OK) return s;
+  if (layer < 0 || layer >= cache->num_layers) return HSTU_ERR_INVALID_ARGUMENT;
+  if (chunk->batch == 0 || chunk->total_tokens == 0) return HSTU_OK;
+  const int64_t hv = static_cast<int64_t>(cache->num_heads) * ATT_HD;
+  const int64_t vec = 16 / static_cast<int64_t>(cache_elt(cache));
+  if (k == nullptr || v == nullptr || !aligned16(k) || !aligned16(v) || ldk < hv || ldv < hv ||
+      ldk % vec != 0 || ldv % vec != 0)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  return launch_append(cache, layer, chunk, seq_ids, k, ldk, v, ldv, nullptr,
+                       static_cast<cudaStream_t>(stream));
+}
+
+hstu_status_t hstu_cache_gather(const hstu_cache_t* cache, int32_t batch, const int32_t* seq_ids,
+                                const int64_t* offsets, int64_t total, void* kv_out,
+                                int64_t* timestamps_out, void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, false)) != HSTU_OK) return s;
+  if (batch < 0 || total < 0 || (batch > 0 && offsets == nullptr)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (batch > 65535) return HSTU_ERR_UNSUPPORTED;
+  if (batch == 0 || total == 0) return HSTU_OK;
+  if (kv_out == nullptr || !aligned16(kv_out)) return HSTU_ERR_INVALID_ARGUMENT;
+  DeviceInfo* di = nullptr;
+  if ((s = device_info(&di)) != HSTU_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t longest = std::min<int64_t>(total, static_cast<int64_t>(cache->max_blocks) * cache->page_size);
+  const dim3 grid(mover_blocks(di->sm_count, longest, static_cast<int64_t>(batch) * cache->num_layers), batch,
+                  cache->num_layers);
+  ProfScope prof(K_CACHE_ROWS, st);
+  hstu_cache_gather_kernel<<<grid, CACHE_COPY_THREADS, 0, st>>>(
+      view_of(cache), seq_ids, offsets, total, static_cast<uint8_t*>(kv_out), timestamps_out);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+hstu_status_t hstu_cache_fork(const hstu_cache_t* cache, int32_t count, const int32_t* src_ids,
+                              const int32_t* dst_ids, void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, true)) != HSTU_OK) return s;
+  if (count < 0 || (count > 0 && (src_ids == nullptr || dst_ids == nullptr)))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (count == 0) return HSTU_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ProfScope prof(K_CACHE_META, st);
+  hstu_cache_fork_kernel<<<count, 128, 0, st>>>(view_of(cache), src_ids, dst_ids);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+hstu_status_t hstu_cache_release(const hstu_cache_t* cache, int32_t count, const int32_t* seq_ids,
+                                 int32_t window, int32_t sinks, void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, true)) != HSTU_OK) return s;
+  if (count < 0 || window < 0 || sinks < 0 || (count > 0 && seq_ids == nullptr))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (count == 0) return HSTU_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ProfScope prof(K_CACHE_META, st);
+  hstu_cache_release_kernel<<<count, 128, 0, st>>>(view_of(cache), seq_ids, window > 0 ? window : -1,
+                                                   sinks);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+hstu_status_t hstu_cache_compact(const hstu_cache_t* cache, int32_t* live_out, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  hstu_status_t s;
+  if ((s = check_cache(cache, true)) != HSTU_OK) return s;
+  if (!aligned16(workspace)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (workspace == nullptr || ws_bytes < cache_ws_bytes(cache, 0)) return HSTU_ERR_WORKSPACE_TOO_SMALL;
+  DeviceInfo* di = nullptr;
+  if ((s = device_info(&di)) != HSTU_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t pages = align_up(static_cast<size_t>(cache->num_pages) * 4, 256);
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  CompactWs ws;
+  ws.count = reinterpret_cast<int32_t*>(b);
+  ws.src = reinterpret_cast<int32_t*>(b + 256);
+  ws.dst = reinterpret_cast<int32_t*>(b + 256 + pages);
+  ws.map = reinterpret_cast<int32_t*>(b + 256 + 2 * pages);
+  ProfScope prof(K_CACHE_META, st);
+  const CacheView v = view_of(cache);
+  hstu_cache_compact_kernel<<<1, CACHE_META_THREADS, 0, st>>>(v, ws, live_out);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  hstu_cache_compact_rows_kernel<<<di->sm_count * 8, CACHE_COPY_THREADS, 0, st>>>(v, ws);
+  HSTU_CHECK_CUDA(cudaGetLastError());
+  return HSTU_OK;
+}
+
+namespace {
+
+hstu_status_t check_paged(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                          const hstu_jagged_t* chunk, int32_t max_context, int32_t window,
+                          int32_t sinks) {
+  hstu_status_t s;
+  if ((s = check_cfg(cfg)) != HSTU_OK) return s;
+  if ((s = check_cache(cache, false)) != HSTU_OK) return s;
+  if ((s = check_chunk(chunk)) != HSTU_OK) return s;
+  if (cache->num_heads != cfg->num_heads || max_context < 0 || window < 0 || sinks < 0)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (chunk->total_tokens > 0 && max_context == 0) return HSTU_ERR_INVALID_ARGUMENT;
+  if (sinks > (1 << 30) || window > (1 << 30)) return HSTU_ERR_UNSUPPORTED;
+  return HSTU_OK;
+}
+
+hstu_status_t paged_attn_entry(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache, int32_t layer,
+                               const hstu_jagged_t* chunk, const int32_t* seq_ids, int32_t max_context,
+                               int32_t window, int32_t sinks, const void* q, int64_t ldq,
+                               const float* rab_pos, const float* rab_time, void* av, float* av_f32,
+                               cudaStream_t st) {
+  hstu_status_t s = check_paged(cfg, cache, chunk, max_context, window, sinks);
+  if (s != HSTU_OK) return s;
+  if (cache->dtype != cfg->dtype || layer < 0 || layer >= cache->num_layers)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (chunk->batch == 0 || chunk->total_tokens == 0) return HSTU_OK;
+  const int64_t hv = static_cast<int64_t>(cfg->num_heads) * ATT_HD;
+  const int64_t vec = 16 / static_cast<int64_t>(cache_elt(cache));
+  if (q == nullptr || rab_pos == nullptr || rab_time == nullptr || (av == nullptr && av_f32 == nullptr) ||
+      !aligned16(q) || !aligned16(av) || !aligned16(av_f32) || ldq < hv || ldq % vec != 0)
+    return HSTU_ERR_INVALID_ARGUMENT;
+  const PagedJob j{cache, chunk, seq_ids, max_context, window, sinks, nullptr};
+  return launch_paged_attn(cfg, j, layer, q, ldq, rab_pos, rab_time, av, av_f32, nullptr, st);
+}
+
+}  // namespace
+
+hstu_status_t hstu_paged_attn_fwd(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                  int32_t layer, const hstu_jagged_t* chunk,
+                                  const int32_t* seq_ids, int32_t max_context, int32_t window,
+                                  int32_t sinks, const void* q, int64_t ldq, const float* rab_pos,
+                                  const float* rab_time, void* av_out, void* stream) {
+  const bool f32 = cfg != nullptr && cfg->dtype == HSTU_FP32;
+  return paged_attn_entry(cfg, cache, layer, chunk, seq_ids, max_context, window, sinks, q, ldq, rab_pos,
+                          rab_time, f32 ? nullptr : av_out, f32 ? static_cast<float*>(av_out) : nullptr,
+                          static_cast<cudaStream_t>(stream));
+}
+
+hstu_status_t hstu_paged_attn_fwd_f32(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                      int32_t layer, const hstu_jagged_t* chunk,
+                                      const int32_t* seq_ids, int32_t max_context, int32_t window,
+                                      int32_t sinks, const void* q, int64_t ldq,
+                                      const float* rab_pos, const float* rab_time, float* av_out,
+                                      void* stream) {
+  return paged_attn_entry(cfg, cache, layer, chunk, seq_ids, max_context, window, sinks, q, ldq, rab_pos,
+                          rab_time, nullptr, av_out, static_cast<cudaStream_t>(stream));
+}
+
+size_t hstu_extend_workspace_bytes(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                   int32_t batch, int64_t total_tokens) {
+  if (check_layer_cfg(cfg) != HSTU_OK || check_cache(cache, false) != HSTU_OK || total_tokens < 0 ||
+      batch < 0)
+    return 0;
+  return layer_ws_bytes(cfg, total_tokens) + stream_ws_bytes(cfg, total_tokens) +
+         cache_ws_bytes(cache, batch);
+}
+
+hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
+                          const hstu_layer_weights_t* weights, const hstu_cache_t* cache,
+                          const hstu_jagged_t* chunk, const int32_t* seq_ids, int32_t max_context,
+                          int32_t window, int32_t sinks, const void* x_in, float* y_out,
+                          void* workspace, size_t ws_bytes, void* stream) {
+  hstu_status_t s;
+  if ((s = check_layer_cfg(cfg)) != HSTU_OK) return s;
+  if ((s = check_paged(cfg, cache, chunk, max_context, window, sinks)) != HSTU_OK) return s;
+  if ((s = check_cache(cache, true)) != HSTU_OK) return s;
+  if (num_layers < 1 || weights == nullptr || cache->num_layers != num_layers ||
+      cache->dtype != (cfg->dtype == HSTU_BF16 ? HSTU_FP16 : HSTU_FP32))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  for (int l = 0; l < num_layers; ++l)
+    if ((s = check_weights(cfg, &weights[l])) != HSTU_OK) return s;
+  const int64_t T = chunk->total_tokens;
+  if (T == 0 || chunk->batch == 0) return HSTU_OK;
+  if (x_in == nullptr || y_out == nullptr || !aligned16(x_in) || !aligned16(y_out) || !aligned16(workspace))
+    return HSTU_ERR_INVALID_ARGUMENT;
+  if (workspace == nullptr || ws_bytes < hstu_extend_workspace_bytes(cfg, cache, chunk->batch, T))
+    return HSTU_ERR_WORKSPACE_TOO_SMALL;
+  const int d = cfg->d_model;
+  const size_t lw = layer_ws_bytes(cfg, T);
+  uint8_t* sp = static_cast<uint8_t*>(workspace) + lw;
+  const size_t fbytes = align_up(static_cast<size_t>(T) * d * 4, 256);
+  const size_t lbytes = align_up(static_cast<size_t>(T) * d * elt(cfg), 256);
+  float* yf[2] = {reinterpret_cast<float*>(sp), reinterpret_cast<float*>(sp + fbytes)};
+  void* yl[2] = {sp + 2 * fbytes, sp + 2 * fbytes + lbytes};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const ReserveWs rws = carve_reserve(cache, chunk->batch, sp + stream_ws_bytes(cfg, T));
+  if ((s = launch_reserve(cache, chunk, seq_ids, rws, st)) != HSTU_OK) return s;
+  const PagedJob pj{cache, chunk, seq_ids, max_context, window, sinks, rws.state};
+  AttnJob base;
+  std::memset(&base, 0, sizeof(base));
+  base.cfg = cfg;
+  base.paged = &pj;
+  const LayerWs ws = carve_layer(cfg, T, workspace);
+  for (int l = 0; l < num_layers; ++l) {
+    const bool last = (l == num_layers - 1);
+    const float* xres = (l == 0) ? nullptr : yf[(l - 1) & 1];
+    float* yo = last ? y_out : yf[l & 1];
+    base.paged_layer = l;
+    if (cfg->dtype == HSTU_BF16) {
+      const void* xin = (l == 0) ? x_in : yl[(l - 1) & 1];
+      s = layer_bf16(cfg, &weights[l], base, xin, l > 0, xres, T, yo, last ? nullptr : yl[l & 1], true,
+                     nullptr, ws, false, st);
+    } else {
+      const float* xin = (l == 0) ? static_cast<const float*>(x_in) : yf[(l - 1) & 1];
+      s = layer_fp32(cfg, &weights[l], base, xin, xres, T, yo, nullptr, ws, false, st);
+    }
+    if (s != HSTU_OK) return s;
+  }
   return HSTU_OK;
 }
 

@@ -1,0 +1,791 @@
+// Attention of a chunk of new events over the paged history cache (cache.cuh):
+// Eq. 2 of the review of "Actions Speak Louder than Words" (section 三 核心公式)
+// for the last c events of a sequence of n, which attend to all n cached events up
+// to themselves:
+//   AV_i = sum_j phi2(q_i.k_j + rab_pos[h, min(i-j, P-1)] + rab_time[h, bt(t_i-t_j)]) v_j / n
+// with a window W (0: none) only over j > i - W and the first `sinks` events;
+// phi2 = softmax replaces phi2 and 1/n by a softmax over the visible keys.
+//
+// What bounds it: every visible K and V row is read once per group of query rows
+// (256 bytes per key and head in 16 bits), so few rows are bound by the cache
+// bandwidth and many rows by the element work per (row, key) pair.  One row over n
+// keys is one row of CTAs, so the keys are split over the CTAs of a thread-block
+// cluster; the partial sums meet in distributed shared memory, in rank order:
+// one launch, no workspace, and the same bits every run.
+//
+// Positions and times: position biases of a key tile are a band of
+// rab_pos (i - j runs over keys + rows - 1 values), loaded per tile, so neither
+// the sequence length nor the table has to fit shared memory.  Times are int32
+// seconds relative to the last event (offset so that they stay non-negative); a
+// visible key 2^31 - 3 seconds or more before it is reported.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "attn.cuh"
+
+namespace hstu {
+
+struct PagedParams {
+  const uint8_t* kv;         // the layer's [num_pages, 2, H, ps, 64]
+  const int64_t* ts;         // [num_pages, ps]
+  const int32_t* table;      // [num_seqs, max_blocks]
+  const int32_t* lengths;    // [num_seqs]
+  const int32_t* seq_ids;    // [B] or nullptr (identity)
+  const int64_t* q_offsets;  // [B + 1]
+  const int64_t* q_ts;       // [T] timestamps of the new events
+  const void* q;             // [T, ldq] operand type
+  int64_t ldq;
+  const float* rab_pos;      // [H, P]
+  const float* rab_time;     // [H, Tb]
+  void* av;                  // [T, H * 64] operand type, or
+  float* av_f32;             // [T, H * 64] fp32
+  float* ln_part;            // [T, H, 2] (sum, centred sum of squares) or nullptr
+  int64_t T;
+  int32_t B, H, P, Tb, num_pages, num_seqs, max_blocks, ps_log2;
+  int32_t max_new, max_context, window, sinks;
+  int32_t groups;            // row groups per sequence
+  int32_t nsplit;            // CTAs of a cluster
+  uint64_t timeout_ns;
+  int32_t thr[MAX_TIME_BUCKETS];  // time-bucket thresholds clamped to int32
+  int4 oct[32];
+};
+
+constexpr int PG_KEYS = 64;  // keys per tile
+
+// One sequence's part of a launch, the same for every CTA of its clusters.
+struct PagedSeq {
+  int seq, n, c;       // table row, events, new events
+  int64_t q0;          // first query row
+  int lo;              // keys [0, sink_end) and [lo, n) are visible to some row
+  int sink_end;
+  int n_sink, first;   // key tiles 0 .. n_sink-1, then first .. first + n_main - 1
+  int n_tiles;
+
+  __device__ __forceinline__ int tile(int k) const { return k < n_sink ? k : first + (k - n_sink); }
+  // whether some row of the chunk sees position j
+  __device__ __forceinline__ bool seen(int j) const {
+    return (j < sink_end || j >= lo) && j < n;
+  }
+};
+
+// Reads and checks sequence u; r0 / r1: the query rows [r0, r1) of this row group.
+// Returns 1 to go on, 0 when the group has no rows, -1 when the input is bad.
+__device__ __forceinline__ int paged_seq(const PagedParams& p, int u, int r0, int rows, PagedSeq& s) {
+  const int64_t o0 = p.q_offsets[u], o1 = p.q_offsets[u + 1];
+  const int64_t cnt = o1 - o0;
+  if (cnt == 0) return 0;
+  s.seq = p.seq_ids != nullptr ? p.seq_ids[u] : u;
+  if (static_cast<uint32_t>(s.seq) >= static_cast<uint32_t>(p.num_seqs)) return -1;
+  s.n = p.lengths[s.seq];
+  if (cnt < 0 || cnt > p.max_new || o0 < 0 || o1 > p.T || s.n < cnt || s.n > p.max_context) return -1;
+  s.c = static_cast<int>(cnt);
+  s.q0 = o0;
+  if (r0 >= s.c) return 0;
+  const int i0 = s.n - s.c + r0;                   // first row's position
+  const int i1 = s.n - s.c + min(r0 + rows, s.c);  // one past the last row's
+  s.lo = p.window > 0 ? max(0, i0 - p.window + 1) : 0;
+  s.sink_end = min(p.sinks, s.lo);
+  s.first = s.lo / PG_KEYS;
+  s.n_sink = min((s.sink_end + PG_KEYS - 1) / PG_KEYS, s.first);
+  s.n_tiles = s.n_sink + (i1 + PG_KEYS - 1) / PG_KEYS - s.first;
+  s.n = i1;  // keys past the group's last row are seen by none of its rows
+  return 1;
+}
+
+// Seconds relative to the last event, shifted into [0, 2^31 - 3].
+constexpr int32_t PG_T0 = INT32_MAX - 2;
+__device__ __forceinline__ int32_t paged_rel(int64_t t, int64_t t_last) {
+  const int64_t d = t - t_last + PG_T0;
+  return d < 0 ? 0 : (d > PG_T0 ? PG_T0 : static_cast<int32_t>(d));
+}
+
+// ---------------------------------------------------------------- fp32
+
+// fp32 layers are small (tens to hundreds of events, one or two heads): FFMA over
+// 64-key tiles in shared memory, 16 query rows per CTA, thread (key or column
+// tid % 64, rows tid / 64 + 4 k).  Exact exponentials (expf), so the result holds
+// fp32 accuracy.  Softmax keeps a running maximum and sum per row.
+constexpr int PG32_ROWS = 16;
+constexpr int PG32_THREADS = 256;
+
+struct Paged32Smem {
+  float q[PG32_ROWS][64];
+  float k[PG_KEYS][65];
+  float v[PG_KEYS][64];
+  float s[PG32_ROWS][PG_KEYS + 1];
+  float o[PG32_ROWS][64];       // this CTA's partial sums
+  float2 ml[PG32_ROWS];         // softmax: (max, sum) of this CTA's keys
+  float scale[PG32_ROWS];       // softmax: factor of the running sums
+  int32_t kt[PG_KEYS];
+  int32_t qt[PG32_ROWS];
+  float rt[MAX_TIME_BUCKETS];
+};
+
+__global__ void __launch_bounds__(PG32_THREADS)
+hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
+  __shared__ Paged32Smem sm;
+  namespace cg = cooperative_groups;
+  const int split = static_cast<int>(blockIdx.x % p.nsplit);
+  const int64_t id = blockIdx.x / p.nsplit;
+  const int h = static_cast<int>(id % p.H);
+  const int g = static_cast<int>((id / p.H) % p.groups), u = static_cast<int>(id / p.H / p.groups);
+  const int tid = threadIdx.x;
+  PagedSeq s;
+  const int r0 = g * PG32_ROWS;
+  const int go = paged_seq(p, u, r0, PG32_ROWS, s);
+  if (go <= 0) {  // the same for the whole cluster
+    if (go < 0 && tid == 0) record_status(HSTU_ERR_DEVICE_CHECK);
+    return;
+  }
+  const bool softmax = phi2 == HSTU_ACT_SOFTMAX;
+  const int rows = min(PG32_ROWS, s.c - r0);
+  const int n_all = p.lengths[s.seq];
+  const int i0 = n_all - s.c + r0;
+  const int64_t t_last = p.q_ts[s.q0 + s.c - 1];
+  const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
+  const int ps = 1 << p.ps_log2;
+  for (int e = tid; e < PG32_ROWS * 64; e += PG32_THREADS) {
+    const int r = e >> 6, c = e & 63;
+    sm.q[r][c] = r < rows ? static_cast<const float*>(p.q)[(s.q0 + r0 + r) * p.ldq + h * 64 + c] : 0.0f;
+  }
+  for (int e = tid; e < p.Tb; e += PG32_THREADS) sm.rt[e] = p.rab_time[static_cast<int64_t>(h) * p.Tb + e];
+  if (tid < PG32_ROWS) {
+    sm.qt[tid] = tid < rows ? paged_rel(p.q_ts[s.q0 + r0 + tid], t_last) : 0;
+    sm.ml[tid] = make_float2(-INFINITY, 0.0f);
+  }
+  const int col = tid & 63, rg = tid >> 6;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
+  const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
+  const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
+  for (int kk = k_begin; kk < k_end; ++kk) {
+    const int j0 = s.tile(kk) * PG_KEYS;
+    __syncthreads();
+    // the tile's rows, 16 bytes per thread and step; keys that no row sees are zeros
+    for (int e = tid; e < 2 * PG_KEYS * 16; e += PG32_THREADS) {
+      const int kv = e >> 10, r = (e >> 4) & 63, c4 = e & 15;
+      const int j = j0 + r;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s.seen(j)) {
+        const int page = tab[j >> p.ps_log2];
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages))
+          x = reinterpret_cast<const float4*>(p.kv)[
+              (((static_cast<int64_t>(page) * 2 + kv) * p.H + h) * ps + (j & (ps - 1))) * 16 + c4];
+        else if (c4 == 0)
+          record_status(HSTU_ERR_DEVICE_CHECK);
+      }
+      if (kv == 0) {
+        sm.k[r][4 * c4] = x.x;
+        sm.k[r][4 * c4 + 1] = x.y;
+        sm.k[r][4 * c4 + 2] = x.z;
+        sm.k[r][4 * c4 + 3] = x.w;
+      } else {
+        *reinterpret_cast<float4*>(&sm.v[r][4 * c4]) = x;
+      }
+    }
+    if (tid < PG_KEYS) {
+      const int j = j0 + tid;
+      int32_t t = 0;
+      if (s.seen(j)) {
+        const int page = tab[j >> p.ps_log2];
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
+          const int64_t tj = p.ts[static_cast<int64_t>(page) * ps + (j & (ps - 1))];
+          if (tj - t_last + PG_T0 < 0) record_status(HSTU_ERR_DEVICE_CHECK);
+          t = paged_rel(tj, t_last);
+        }
+      }
+      sm.kt[tid] = t;
+    }
+    __syncthreads();
+    const int j = j0 + col;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int r = rg + 4 * a;
+      float dot = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 64; ++c) dot = fmaf(sm.q[r][c], sm.k[col][c], dot);
+      const int i = i0 + r;
+      const bool vis = r < rows && j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
+      float x = dot;
+      if (vis) {
+        const int b = time_bucket_octave(sm.qt[r] - sm.kt[col], p.oct);
+        x += rp[min(i - j, p.P - 1)] + sm.rt[b];
+      }
+      sm.s[r][col] = softmax ? (vis ? x : -INFINITY) : (vis ? phi_runtime(x, phi2) : 0.0f);
+    }
+    __syncthreads();
+    if (softmax) {
+      if (tid < PG32_ROWS) {
+        float m = sm.ml[tid].x;
+        for (int c = 0; c < PG_KEYS; ++c) m = fmaxf(m, sm.s[tid][c]);
+        const float f = m > -INFINITY ? expf(sm.ml[tid].x - m) : 1.0f;
+        float l = sm.ml[tid].y * f;
+        for (int c = 0; c < PG_KEYS; ++c) {
+          const float e = m > -INFINITY ? expf(sm.s[tid][c] - m) : 0.0f;
+          sm.s[tid][c] = e;
+          l += e;
+        }
+        sm.scale[tid] = f;
+        sm.ml[tid] = make_float2(m, l);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int a = 0; a < 4; ++a) acc[a] *= sm.scale[rg + 4 * a];
+    }
+    // each tile's sum apart, then added: the rounding grows with the tiles, not the keys
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < PG_KEYS; ++c) {
+      const float vv = sm.v[c][col];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) part[a] = fmaf(sm.s[rg + 4 * a][c], vv, part[a]);
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a) acc[a] += part[a];
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) sm.o[rg + 4 * a][col] = acc[a];
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  // rank `split` writes rows split, split + nsplit, ...: 64 threads per row
+  for (int r = split * 4 + rg; r < rows; r += 4 * p.nsplit) {
+    float o = 0.0f;
+    if (softmax) {
+      float m = -INFINITY, l = 0.0f;
+      for (int k = 0; k < p.nsplit; ++k) m = fmaxf(m, cluster.map_shared_rank(&sm, k)->ml[r].x);
+      for (int k = 0; k < p.nsplit; ++k) {
+        const Paged32Smem* o_sm = cluster.map_shared_rank(&sm, k);
+        const float f = o_sm->ml[r].x > -INFINITY ? expf(o_sm->ml[r].x - m) : 0.0f;
+        l += o_sm->ml[r].y * f;
+        o += o_sm->o[r][col] * f;
+      }
+      o = l > 0.0f ? o / l : 0.0f;
+    } else {
+      for (int k = 0; k < p.nsplit; ++k) o += cluster.map_shared_rank(&sm, k)->o[r][col];
+      o /= static_cast<float>(n_all);
+    }
+    p.av_f32[((s.q0 + r0 + r) * p.H + h) * 64 + col] = o;
+  }
+  cluster.sync();  // no CTA leaves while another reads its partial sums
+}
+
+// ---------------------------------------------------------------- few rows
+
+// 16-bit operands, 16 * MT query rows per CTA, keys split over a cluster.  Bound
+// by the cache bandwidth, so the tensor work runs on warp-level MMAs (m16n8k16)
+// whose operands and results stay in registers: a 128-row tcgen05 tile would do
+// the element work of 128 rows for the 1..32 that exist.  Warp w of 4 owns keys
+// 16 w .. 16 w + 15 of every 64-key tile for all the rows: S = Q K^T, the element
+// work and O += P V need no exchange between warps until the end.  A fifth warp
+// streams K, V (TMA, one box per page part, 128B swizzle), key times and the
+// position band through a ring of stages; table entries are read two tiles ahead
+// and times one tile ahead, so their latency stays off the ring.
+constexpr int PGS_WARPS = 4;
+constexpr int PGS_THREADS = (PGS_WARPS + 1) * 32;
+constexpr int PGS_STAGES = 4;
+constexpr uint32_t PGS_TILE_BYTES = PG_KEYS * 128;
+constexpr int PGS_OLD = 68;  // row stride (floats) of the partial sums: 16-byte rows, no bank conflicts
+
+struct PgsSmem {
+  static constexpr uint32_t kK = 0;
+  static constexpr uint32_t kV = kK + PGS_STAGES * PGS_TILE_BYTES;
+  static constexpr uint32_t kSide = kV + PGS_STAGES * PGS_TILE_BYTES;  // per stage: 64 times, 96 biases
+  static constexpr uint32_t kSideBytes = 64 * 4 + 96 * 4;
+  static constexpr uint32_t kTime = kSide + PGS_STAGES * kSideBytes;
+  static constexpr uint32_t kThr = kTime + MAX_TIME_BUCKETS * 4;
+  static constexpr uint32_t kOct = kThr + MAX_TIME_BUCKETS * 4;
+  static constexpr uint32_t kOrt = kOct + 32 * 16;
+  static constexpr uint32_t kMl = kOrt + 32 * 16;                  // 4 warps x 32 rows float2
+  static constexpr uint32_t kMlC = kMl + PGS_WARPS * 32 * 8;       // 32 rows float2 of the CTA
+  static constexpr uint32_t kBars = kMlC + 32 * 8;
+  static constexpr uint32_t kAbort = kBars + 2 * PGS_STAGES * 8;
+  static constexpr uint32_t kBytes = kAbort + 16 + 1024;           // + align slack
+  static_assert(PGS_WARPS * 32 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
+};
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), 16-bit operands.
+template <bool F16>
+__device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
+  if constexpr (F16) return pack_h2(lo, hi);
+  else return pack_bf16x2(lo, hi);
+}
+
+// A row's result: 16-bit or fp32, with the row's LayerNorm partial sums on
+// request; the 16 lanes of a half warp hold the row's 64 columns (4 each).
+template <bool F16>
+__device__ __forceinline__ void paged_store(const PagedParams& p, int64_t row, int h, int c4, float4 o,
+                                            bool live) {
+  const int64_t at = (row * p.H + h) * 64 + 4 * c4;
+  if (live) {
+    if (p.av_f32 != nullptr)
+      *reinterpret_cast<float4*>(p.av_f32 + at) = o;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.av) + at) =
+          make_uint2(pack_16<F16>(o.x, o.y), pack_16<F16>(o.z, o.w));
+  }
+  if (p.ln_part != nullptr) {  // uniform; every lane of the warp takes part
+    float sum = o.x + o.y + o.z + o.w;
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    const float m = sum * (1.0f / 64.0f);
+    float sq = (o.x - m) * (o.x - m) + (o.y - m) * (o.y - m) + (o.z - m) * (o.z - m) + (o.w - m) * (o.w - m);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, d);
+    if (live && c4 == 0)
+      reinterpret_cast<float2*>(p.ln_part)[row * p.H + h] = make_float2(sum, sq);
+  }
+}
+
+template <int PHI, bool F16, int MT>
+__global__ void __launch_bounds__(PGS_THREADS)
+hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ PagedParams p) {
+  constexpr int R = 16 * MT;
+  constexpr bool kSoftmax = PHI == HSTU_ACT_SOFTMAX;
+  constexpr float kScale = phi_scale<PHI>();
+  constexpr int kBand = PG_KEYS + R;  // biases of a tile (one unused)
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  namespace cg = cooperative_groups;
+  // the same offset in every CTA of a cluster: shared memory is read across it
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int split = static_cast<int>(blockIdx.x % p.nsplit);
+  const int64_t id = blockIdx.x / p.nsplit;
+  const int h = static_cast<int>(id % p.H);
+  const int g = static_cast<int>((id / p.H) % p.groups), u = static_cast<int>(id / p.H / p.groups);
+  const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
+  PagedSeq s;
+  const int r0 = g * R;
+  const int go = paged_seq(p, u, r0, R, s);
+  if (go <= 0) {  // the same for the whole cluster, before any barrier
+    if (go < 0 && tid == 0) record_status(HSTU_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int rows = min(R, s.c - r0);
+  const int n_all = p.lengths[s.seq];
+  const int i0 = n_all - s.c + r0;  // position of the group's first row
+  const int64_t t_last = p.q_ts[s.q0 + s.c - 1];
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + PgsSmem::kBars);
+  uint64_t* bar_empty = bar_full + PGS_STAGES;
+  volatile int* sAbort = reinterpret_cast<volatile int*>(smem + PgsSmem::kAbort);
+  float* sTime = reinterpret_cast<float*>(smem + PgsSmem::kTime);
+  int32_t* sThr = reinterpret_cast<int32_t*>(smem + PgsSmem::kThr);
+  int4* sOct = reinterpret_cast<int4*>(smem + PgsSmem::kOct);
+  float4* sOrt = reinterpret_cast<float4*>(smem + PgsSmem::kOrt);
+  float2* sMl = reinterpret_cast<float2*>(smem + PgsSmem::kMl);
+  float2* sMlC = reinterpret_cast<float2*>(smem + PgsSmem::kMlC);
+  if (tid == 0) {
+    for (int k = 0; k < PGS_STAGES; ++k) {
+      mbar_init(&bar_full[k], 2);
+      mbar_init(&bar_empty[k], PGS_WARPS);
+    }
+    *sAbort = 0;
+    fence_mbar_init();
+  }
+  const float* rt_g = p.rab_time + static_cast<int64_t>(h) * p.Tb;
+  for (int k = tid; k < p.Tb; k += PGS_THREADS) {
+    sTime[k] = kScale * rt_g[k];
+    sThr[k] = p.thr[k];
+  }
+  if (tid < 32) {
+    const int4 o = p.oct[tid];
+    auto tb = [&](int b) { return kScale * rt_g[min(max(b, 0), p.Tb - 1)]; };
+    sOct[tid] = o;
+    sOrt[tid] = make_float4(tb(o.w), tb(o.w + 1), tb(o.w + 2), tb(o.w + 3));
+  }
+  __syncthreads();
+  const WaitCtl ctl{sAbort, p.timeout_ns};
+  const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
+  const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
+
+  if (warp == PGS_WARPS) {
+    // ---------------- producer
+    const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
+    const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
+    const int psl = p.ps_log2, ps = 1 << psl;
+    const int box = min(ps, PG_KEYS), nbox = PG_KEYS / box;
+    const int32_t oob = static_cast<int32_t>((static_cast<int64_t>(p.num_pages) * 2 * p.H) << psl);
+    constexpr int NB = kBand / 32 + (kBand % 32 != 0);
+    // page of the lane's positions j0 + lane and j0 + 32 + lane, -1 where no row
+    // sees the position; a visible position without a page is reported
+    auto load_pages = [&](int kk, int (&pg)[2]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        pg[e] = -1;
+        if (kk < k_end) {
+          const int j = s.tile(kk) * PG_KEYS + lane + 32 * e;
+          if (s.seen(j)) pg[e] = tab[j >> psl];
+        }
+      }
+    };
+    auto load_side = [&](int kk, const int (&pg)[2], int64_t (&t)[2], float (&bd)[NB]) {
+      if (kk >= k_end) return;
+      const int j0 = s.tile(kk) * PG_KEYS;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = j0 + lane + 32 * e;
+        t[e] = t_last;  // past the last row: as the last event
+        if (s.seen(j)) {
+          if (static_cast<uint32_t>(pg[e]) < static_cast<uint32_t>(p.num_pages))
+            t[e] = p.ts[(static_cast<int64_t>(pg[e]) << psl) + (j & (ps - 1))];
+          else
+            record_status(HSTU_ERR_DEVICE_CHECK);
+          if (t_last - t[e] > PG_T0) record_status(HSTU_ERR_DEVICE_CHECK);
+        } else if (j < s.n) {
+          t[e] = t_last - PG_T0;  // a gap below the window: as old as can be
+        }
+      }
+      // entry x: i - j = (i0 + R - 1) - j0 - x, for column c and row r at x = c + R - 1 - r
+#pragma unroll
+      for (int e = 0; e < NB; ++e) {
+        const int x = lane + 32 * e;
+        const int d = i0 + R - 1 - j0 - x;
+        if (x < kBand) bd[e] = kScale * __ldg(rp + min(max(d, 0), p.P - 1));
+      }
+    };
+    int pg0[2], pg1[2], pg2[2];
+    int64_t t0[2], t1[2];
+    float b0[NB], b1[NB];
+    load_pages(k_begin, pg0);
+    load_pages(k_begin + 1, pg1);
+    load_side(k_begin, pg0, t0, b0);
+    int issued = 0;
+    for (int kk = k_begin; kk < k_end; ++kk) {
+      const int st = issued % PGS_STAGES;
+      load_pages(kk + 2, pg2);
+      load_side(kk + 1, pg1, t1, b1);
+      int ok = 0;
+      if (lane == 0) ok = mbar_wait(&bar_empty[st], ((issued / PGS_STAGES) & 1) ^ 1, ctl) ? 1 : 0;
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (lane == 0) mbar_arrive_expect_tx(&bar_full[st], 2 * PGS_TILE_BYTES);
+      __syncwarp();
+      const int j0 = s.tile(kk) * PG_KEYS;
+      // a box's page: the one of its first seen position (parts that no row sees have none)
+      int page = -1;
+      for (int b = 0; b < nbox; ++b) {
+        const unsigned lo = __ballot_sync(0xffffffffu, (lane / box) == b && pg0[0] >= 0);
+        const unsigned hi = __ballot_sync(0xffffffffu, ((lane + 32) / box) == b && pg0[1] >= 0);
+        int v = -1;
+        if (lo) v = __shfl_sync(0xffffffffu, pg0[0], __ffs(lo) - 1);
+        else if (hi) v = __shfl_sync(0xffffffffu, pg0[1], __ffs(hi) - 1);
+        if (lane == b) page = v;
+      }
+      if (lane < nbox) {
+        const int jb = j0 + lane * box;
+        const bool pok = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages);
+        const int32_t row = pok ? static_cast<int32_t>((((static_cast<int64_t>(page) * 2) * p.H + h) << psl) + (jb & (ps - 1))) : oob;
+        const int32_t row_v = pok ? row + (p.H << psl) : oob;
+        uint8_t* dk = smem + PgsSmem::kK + st * PGS_TILE_BYTES + lane * box * 128;
+        tma_load_2d(dk, &tm_kv, &bar_full[st], 0, row);
+        tma_load_2d(dk + (PgsSmem::kV - PgsSmem::kK), &tm_kv, &bar_full[st], 0, row_v);
+      }
+      ++issued;
+      int32_t* side_t = reinterpret_cast<int32_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
+      float* side_b = reinterpret_cast<float*>(side_t + 64);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) side_t[lane + 32 * e] = paged_rel(t0[e], t_last);
+#pragma unroll
+      for (int e = 0; e < NB; ++e)
+        if (lane + 32 * e < kBand) side_b[lane + 32 * e] = b0[e];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_full[st]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        pg0[e] = pg1[e];
+        pg1[e] = pg2[e];
+        t0[e] = t1[e];
+      }
+#pragma unroll
+      for (int e = 0; e < NB; ++e) b0[e] = b1[e];
+    }
+    // every issued load lands before shared memory is reused or released
+    if (lane == 0)
+      for (int k = max(0, issued - PGS_STAGES); k < issued; ++k)
+        mbar_wait_drain(&bar_full[k % PGS_STAGES], (k / PGS_STAGES) & 1, p.timeout_ns);
+    __syncwarp();
+  }
+
+  // ---------------- compute warps
+  float o[MT][8][4];
+  float m_run[2 * MT], l_run[2 * MT];
+#pragma unroll
+  for (int a = 0; a < MT; ++a)
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[a][b][e] = 0.0f;
+#pragma unroll
+  for (int a = 0; a < 2 * MT; ++a) {
+    m_run[a] = -INFINITY;
+    l_run[a] = 0.0f;
+  }
+  const int gr = lane >> 2, tq = lane & 3;  // row and column pair of the MMA fragments
+  if (warp < PGS_WARPS) {
+    uint32_t qf[MT][4][4];
+    int32_t ti[2 * MT], bound[2 * MT];
+    float rt[2 * MT];
+#pragma unroll
+    for (int a = 0; a < 2 * MT; ++a) {  // rows gr + 8 a
+      const int r = gr + 8 * a;
+      const bool in = r < rows;
+      const uint16_t* q = static_cast<const uint16_t*>(p.q) + (s.q0 + r0 + (in ? r : 0)) * p.ldq + h * 64;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[a >> 1][k][(a & 1) + 2 * e] =
+              in ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * e + 2 * tq)) : 0u;
+      ti[a] = in ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
+      bound[a] = -1;  // the first chunk looks its buckets up
+      rt[a] = 0.0f;
+    }
+    const uint32_t sbase = smem_u32(smem);
+    const int wk = warp * 16;  // this warp's keys of a tile
+    // ldmatrix rows of this lane: K (keys, then the two k halves), V (key halves, then columns)
+    const int krow = wk + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
+    const int vrow = wk + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
+    const uint32_t kaddr = sbase + PgsSmem::kK + krow * 128, vaddr = sbase + PgsSmem::kV + vrow * 128;
+    int it = 0;
+    for (int kk = k_begin; kk < k_end; ++kk, ++it) {
+      const int st = it % PGS_STAGES;
+      const bool ok = mbar_wait(&bar_full[st], (it / PGS_STAGES) & 1, ctl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int j0 = s.tile(kk) * PG_KEYS + wk;  // this warp's first key
+      const uint32_t soff = st * PGS_TILE_BYTES;
+      const int32_t* side_t = reinterpret_cast<const int32_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
+      const float* band = reinterpret_cast<const float*>(side_t + 64) + wk + R - 1;
+      // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
+      // times a NaN is a NaN, so they are cleared
+      const bool gap = j0 < s.lo && j0 + 16 > s.sink_end;
+      if (j0 + 16 > s.n || gap) {
+#pragma unroll
+        for (int e = lane; e < 16 * 8; e += 32)
+          if (!s.seen(j0 + (e >> 3)))
+            *reinterpret_cast<uint4*>(smem + PgsSmem::kV + soff + (wk + (e >> 3)) * 128 + (e & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      float sc[MT][2][4];
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t kf[4];
+        ldsm_x4(kaddr + soff + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+          mma_m16n8k16<F16>(sc[a][0], qf[a][k], kf[0], kf[1]);
+          mma_m16n8k16<F16>(sc[a][1], qf[a][k], kf[2], kf[3]);
+        }
+      }
+      // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
+      int2 kt[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) kt[b] = *reinterpret_cast<const int2*>(side_t + wk + 8 * b + 2 * tq);
+      const int32_t kt_end = side_t[wk + 15];
+      bool steady = true;
+#pragma unroll
+      for (int a = 0; a < 2 * MT; ++a) steady = steady && kt_end <= bound[a];
+      // times are not in order across a gap: buckets are looked up there and after it
+      steady = __all_sync(0xffffffffu, steady) && !gap;
+      // every row sees every key of this warp
+      const int i_last = i0 + rows - 1;
+      const bool full = j0 + 15 <= i0 &&
+                        (p.window == 0 || j0 > i_last - p.window || j0 + 16 <= p.sinks);
+      uint32_t pf[MT][4];
+#pragma unroll
+      for (int a = 0; a < 2 * MT; ++a) {
+        const int r = gr + 8 * a;
+        float x[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float* bp = band + 8 * b + 2 * tq - r;
+          float rt0 = rt[a], rt1 = rt[a];
+          if (!steady) {
+            rt0 = time_bias_octave(ti[a] - kt[b].x, sOct, sOrt);
+            rt1 = time_bias_octave(ti[a] - kt[b].y, sOct, sOrt);
+          }
+          x[2 * b] = fmaf(sc[a >> 1][b][2 * (a & 1)], kScale, bp[0] + rt0);
+          x[2 * b + 1] = fmaf(sc[a >> 1][b][2 * (a & 1) + 1], kScale, bp[1] + rt1);
+        }
+        if (!steady) {
+          // the bucket of the chunk's last key holds until a key passes its edge
+          const int bk = time_bucket_octave(ti[a] - kt_end, sOct);
+          rt[a] = sTime[bk];
+          bound[a] = gap ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
+        }
+        const int i = i0 + r;
+        auto vis = [&](int e) {
+          const int j = j0 + 8 * (e >> 1) + 2 * tq + (e & 1);
+          return j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
+        };
+        if constexpr (kSoftmax) {
+          if (!full)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = vis(e) ? x[e] : -INFINITY;
+          float cm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+          cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
+          cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
+          if (__any_sync(0xffffffffu, cm > m_run[a])) {
+            const float mn = fmaxf(m_run[a], cm);
+            const float f = mn > -INFINITY ? ex2_approx(m_run[a] - mn) : 1.0f;
+            m_run[a] = mn;
+            l_run[a] *= f;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              o[a >> 1][b][2 * (a & 1)] *= f;
+              o[a >> 1][b][2 * (a & 1) + 1] *= f;
+            }
+          }
+          const float mm = m_run[a] > -INFINITY ? m_run[a] : 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = ex2_approx(x[e] - mm);
+            l_run[a] += x[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (PHI == HSTU_ACT_SILU) x[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
+            else if constexpr (PHI == HSTU_ACT_RELU) x[e] = fmaxf(x[e], 0.0f);
+            if (!full) x[e] = vis(e) ? x[e] : 0.0f;
+          }
+        }
+        // P in the operand type: the MMA takes both operands in one type
+        pf[a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
+        pf[a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
+      }
+      // ---- O += P V
+#pragma unroll
+      for (int b = 0; b < 8; b += 2) {
+        uint32_t vf[4];
+        ldsm_x4_t(vaddr + soff + (((b + vch) ^ (vrow & 7)) << 4), vf);
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+          mma_m16n8k16<F16>(o[a][b], pf[a], vf[0], vf[1]);
+          mma_m16n8k16<F16>(o[a][b + 1], pf[a], vf[2], vf[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_empty[st]);
+    }
+  }
+  __syncthreads();  // the stages are idle: the partial sums go over them
+  float* sO = reinterpret_cast<float*>(smem);
+  if (warp < PGS_WARPS) {
+#pragma unroll
+    for (int a = 0; a < 2 * MT; ++a) {
+      const int r = gr + 8 * a;
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        *reinterpret_cast<float2*>(sO + (warp * R + r) * PGS_OLD + 8 * b + 2 * tq) =
+            make_float2(o[a >> 1][b][2 * (a & 1)], o[a >> 1][b][2 * (a & 1) + 1]);
+      if constexpr (kSoftmax) {
+        float l = l_run[a];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (tq == 0) sMl[warp * 32 + r] = make_float2(m_run[a], l);
+      }
+    }
+  }
+  __syncthreads();
+  // the CTA's sums over its four warps, in place of warp 0's (8 rows x 16 lanes a step)
+  const bool alone = p.nsplit == 1;
+  const int c4 = tid & 15;
+  const float inv_n = kSoftmax ? 1.0f : 1.0f / static_cast<float>(n_all);
+  if (warp < PGS_WARPS) {
+    for (int r = tid >> 4; r < R; r += 8) {
+      float f[PGS_WARPS], m = -INFINITY, l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < PGS_WARPS; ++w) f[w] = 1.0f;
+      if constexpr (kSoftmax) {
+#pragma unroll
+        for (int w = 0; w < PGS_WARPS; ++w) m = fmaxf(m, sMl[w * 32 + r].x);
+#pragma unroll
+        for (int w = 0; w < PGS_WARPS; ++w) {
+          const float2 v = sMl[w * 32 + r];
+          f[w] = v.x > -INFINITY ? ex2_approx(v.x - m) : 0.0f;
+          l = fmaf(v.y, f[w], l);
+        }
+      }
+      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < PGS_WARPS; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(sO + (w * R + r) * PGS_OLD + 4 * c4);
+        t.x = fmaf(v.x, f[w], t.x);
+        t.y = fmaf(v.y, f[w], t.y);
+        t.z = fmaf(v.z, f[w], t.z);
+        t.w = fmaf(v.w, f[w], t.w);
+      }
+      if (alone) {
+        const float k = kSoftmax ? (l > 0.0f ? 1.0f / l : 0.0f) : inv_n;
+        paged_store<F16>(p, s.q0 + r0 + r, h, c4, make_float4(t.x * k, t.y * k, t.z * k, t.w * k), r < rows);
+      } else {
+        *reinterpret_cast<float4*>(sO + r * PGS_OLD + 4 * c4) = t;  // read by this thread alone before
+        if (kSoftmax && c4 == 0) sMlC[r] = make_float2(m, l);
+      }
+    }
+  }
+  if (alone) return;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  if (warp < PGS_WARPS) {
+    // rank `split` takes rows 8 split .., 8 (split + nsplit) ..
+    for (int r = 8 * split + (tid >> 4); r < R; r += 8 * p.nsplit) {
+      float m = -INFINITY, l = 0.0f;
+      if constexpr (kSoftmax)
+        for (int k = 0; k < p.nsplit; ++k) m = fmaxf(m, cluster.map_shared_rank(sMlC, k)[r].x);
+      float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k = 0; k < p.nsplit; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sO, k) + r * PGS_OLD + 4 * c4);
+        float f = 1.0f;
+        if constexpr (kSoftmax) {
+          const float2 ml = cluster.map_shared_rank(sMlC, k)[r];
+          f = ml.x > -INFINITY ? ex2_approx(ml.x - m) : 0.0f;
+          l = fmaf(ml.y, f, l);
+        }
+        t.x = fmaf(v.x, f, t.x);
+        t.y = fmaf(v.y, f, t.y);
+        t.z = fmaf(v.z, f, t.z);
+        t.w = fmaf(v.w, f, t.w);
+      }
+      const float k = kSoftmax ? (l > 0.0f ? 1.0f / l : 0.0f) : inv_n;
+      paged_store<F16>(p, s.q0 + r0 + r, h, c4, make_float4(t.x * k, t.y * k, t.z * k, t.w * k), r < rows);
+    }
+  }
+  cluster.sync();  // no CTA leaves while another reads its partial sums
+}
+
+}  // namespace hstu

@@ -56,10 +56,23 @@ class KernelTimeT(ctypes.Structure):
                 ("total_ms", ctypes.c_double)]
 
 
+class CacheT(ctypes.Structure):
+    _fields_ = [("num_layers", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("kv", ctypes.c_void_p),
+                ("timestamps", ctypes.c_void_p), ("ref_count", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("lengths", ctypes.c_void_p)]
+
+
 class LayerWeightsT(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("w1", "b1", "w2", "b2", "rab_pos", "rab_time", "ln_gamma", "ln_beta")]
 
+
+_PAGED_ATTN_ARGS = ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                     ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 4)
 
 EXPORTS = {
     "hstu_version": (ctypes.c_char_p, []),
@@ -89,6 +102,24 @@ EXPORTS = {
     "hstu_stochastic_length": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
                                               ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64]
                                + [ctypes.c_void_p] * 7),
+    "hstu_cache_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_int32]),
+    "hstu_cache_reserve": (ctypes.c_int, [ctypes.c_void_p] * 4 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "hstu_cache_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                         ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    "hstu_cache_gather": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_int64] + [ctypes.c_void_p] * 3),
+    "hstu_cache_fork": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 3),
+    "hstu_cache_release": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                          ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]),
+    "hstu_cache_compact": (ctypes.c_int, [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "hstu_paged_attn_fwd": (ctypes.c_int, _PAGED_ATTN_ARGS),
+    "hstu_paged_attn_fwd_f32": (ctypes.c_int, _PAGED_ATTN_ARGS),
+    "hstu_extend_workspace_bytes": (ctypes.c_size_t, [ctypes.c_void_p, ctypes.c_void_p,
+                                                      ctypes.c_int32, ctypes.c_int64]),
+    "hstu_extend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32] + [ctypes.c_void_p] * 4
+                    + [ctypes.c_int32] * 3 + [ctypes.c_void_p] * 3
+                    + [ctypes.c_size_t, ctypes.c_void_p]),
     "hstu_get_device_status": (ctypes.c_int, [ctypes.c_void_p]),
     "hstu_profiler_start": (ctypes.c_int, []),
     "hstu_profiler_stop": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
@@ -420,6 +451,172 @@ def stochastic_length(jag: Jagged, alpha: float, seed: int, step: int, x=None, s
     return out
 
 
+@dataclass
+class PagedCache:
+    """A paged history cache: the caller's five device tensors (see hstu_cache_t)."""
+    kv: torch.Tensor           # [L, num_pages, 2, H, page_size, 64], the cache type
+    timestamps: torch.Tensor   # int64 [num_pages, page_size]
+    ref_count: torch.Tensor    # int32 [num_pages]
+    block_table: torch.Tensor  # int32 [num_seqs, max_blocks], -1 = no page
+    lengths: torch.Tensor      # int32 [num_seqs]
+
+    @staticmethod
+    def empty(num_layers: int, num_heads: int, num_pages: int, num_seqs: int, max_blocks: int,
+              page_size: int = 64, dtype: str = "fp16", device="cuda") -> "PagedCache":
+        """A new cache with every page free.  The pages are not initialised: no
+        call reads a slot that was not written."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return PagedCache(
+            torch.empty((num_layers, num_pages, 2, num_heads, page_size, 64),
+                        dtype=TORCH_DTYPE[dtype], device=device),
+            torch.empty((num_pages, page_size), dtype=torch.int64, device=device),
+            torch.zeros(num_pages, **i32), torch.full((num_seqs, max_blocks), -1, **i32),
+            torch.zeros(num_seqs, **i32))
+
+    def c(self) -> CacheT:
+        L, pages, _, H, ps, _ = self.kv.shape
+        return CacheT(L, H, _CACHE_DTYPE[self.kv.dtype], ps, pages, self.lengths.shape[0],
+                      self.block_table.shape[1], self.kv.data_ptr(), self.timestamps.data_ptr(),
+                      self.ref_count.data_ptr(), self.block_table.data_ptr(),
+                      self.lengths.data_ptr())
+
+
+_CACHE_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
+def cache_workspace_bytes(cache: PagedCache, batch: int) -> int:
+    return lib().hstu_cache_workspace_bytes(ctypes.byref(cache.c()), batch)
+
+
+def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None, stream=None):
+    """Make room for the chunk's new events (chunk.offsets: their row ranges per
+    sequence) and lengthen the sequences; shared partial last pages are copied.
+    A pool that is too small leaves everything as it was and is reported in
+    device_status()."""
+    c, j = cache.c(), chunk.c()
+    if workspace is None:
+        nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), j.batch)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.kv.device)
+    _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j), _p(seq_ids), _p(workspace),
+                                    workspace.numel(), _stream(stream)), "hstu_cache_reserve")
+
+
+def _rows_ld(t: torch.Tensor, what: str) -> int:
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: rows of contiguous elements are needed")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def cache_append(cache: PagedCache, layer: int, chunk: Jagged, k, v, seq_ids=None, stream=None):
+    """Write K and V ([T, H*64], any row stride) of the chunk's rows into a layer's pages."""
+    if k.dtype != cache.kv.dtype or v.dtype != cache.kv.dtype:
+        raise ValueError("cache_append: k and v must have the cache's type")
+    c, j = cache.c(), chunk.c()
+    _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j), _p(seq_ids), _p(k),
+                                   _rows_ld(k, "k"), _p(v), _rows_ld(v, "v"), _stream(stream)),
+           "hstu_cache_append")
+
+
+def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=None, stream=None):
+    """Whole sequences out of their pages: returns (kv [L, total, 2*H*64] in the
+    layout of forward()'s kv_cache_out, timestamps [total])."""
+    L, _, _, H, _, _ = cache.kv.shape
+    if kv_out is None:
+        kv_out = torch.empty((L, total, 2 * H * 64), dtype=cache.kv.dtype, device=cache.kv.device)
+    ts = torch.empty(total, dtype=torch.int64, device=cache.kv.device)
+    _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), offsets.numel() - 1, _p(seq_ids),
+                                   _p(offsets), total, _p(kv_out), _p(ts), _stream(stream)),
+           "hstu_cache_gather")
+    return kv_out, ts
+
+
+def cache_fork(cache: PagedCache, src_ids, dst_ids, stream=None):
+    """dst_ids[i] (an empty sequence) becomes a copy of src_ids[i] sharing its pages."""
+    if src_ids.numel() != dst_ids.numel():
+        raise ValueError("cache_fork: one destination per source")
+    _check(lib().hstu_cache_fork(ctypes.byref(cache.c()), src_ids.numel(), _p(src_ids),
+                                 _p(dst_ids), _stream(stream)), "hstu_cache_fork")
+
+
+def cache_release(cache: PagedCache, seq_ids, window: int = 0, sinks: int = 0, stream=None):
+    """Release whole sequences, or with a window the pages that no later event sees."""
+    _check(lib().hstu_cache_release(ctypes.byref(cache.c()), seq_ids.numel(), _p(seq_ids), window,
+                                    sinks, _stream(stream)), "hstu_cache_release")
+
+
+def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tensor:
+    """Move the used pages into the lowest ids; returns their number (int32 [1], device)."""
+    live = torch.empty(1, dtype=torch.int32, device=cache.kv.device)
+    c = cache.c()
+    if workspace is None:
+        nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), 0)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.kv.device)
+    _check(lib().hstu_cache_compact(ctypes.byref(c), _p(live), _p(workspace), workspace.numel(),
+                                    _stream(stream)), "hstu_cache_compact")
+    return live
+
+
+def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context, window, sinks,
+                seq_ids, av_out, stream):
+    if q.dtype != cache.kv.dtype:
+        raise ValueError(f"{fn}: q must have the cache's type")
+    c, ca, j = cfg.c(), cache.c(), chunk.c()
+    _check(getattr(lib(), fn)(ctypes.byref(c), ctypes.byref(ca), layer, ctypes.byref(j),
+                              _p(seq_ids), max_context, window, sinks, _p(q), _rows_ld(q, "q"),
+                              _p(rab_pos), _p(rab_time), _p(av_out), _stream(stream)), fn)
+    return av_out
+
+
+def paged_attn_fwd(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagged, q, rab_pos,
+                   rab_time, max_context: int, window: int = 0, sinks: int = 0, seq_ids=None,
+                   av_out=None, stream=None) -> torch.Tensor:
+    """Eq. 2 for the chunk's rows (the last events of their sequences) over the
+    cache: AV [T, H*64] in cfg dtype.  window > 0: a row sees the last `window`
+    events up to itself and the first `sinks` events of its sequence."""
+    if av_out is None:
+        av_out = torch.empty((chunk.total_tokens, cfg.num_heads * cfg.dv), dtype=cfg.torch_dtype,
+                             device=q.device)
+    return _paged_attn("hstu_paged_attn_fwd", cfg, cache, layer, chunk, q, rab_pos, rab_time,
+                       max_context, window, sinks, seq_ids, av_out, stream)
+
+
+def paged_attn_fwd_f32(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagged, q, rab_pos,
+                       rab_time, max_context: int, window: int = 0, sinks: int = 0, seq_ids=None,
+                       av_out=None, stream=None) -> torch.Tensor:
+    """paged_attn_fwd with the result in fp32."""
+    if av_out is None:
+        av_out = torch.empty((chunk.total_tokens, cfg.num_heads * cfg.dv), dtype=torch.float32,
+                             device=q.device)
+    return _paged_attn("hstu_paged_attn_fwd_f32", cfg, cache, layer, chunk, q, rab_pos, rab_time,
+                       max_context, window, sinks, seq_ids, av_out, stream)
+
+
+def extend_workspace_bytes(cfg: LayerConfig, cache: PagedCache, batch: int, total_tokens: int) -> int:
+    return lib().hstu_extend_workspace_bytes(ctypes.byref(cfg.c()), ctypes.byref(cache.c()), batch,
+                                             total_tokens)
+
+
+def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache, chunk: Jagged,
+           x_in, max_context: int, window: int = 0, sinks: int = 0, seq_ids=None, y_out=None,
+           workspace=None, stream=None) -> torch.Tensor:
+    """New events through the stack against the cache (reserve, then per layer f1,
+    append, paged attention, f2); returns Y [T, d] fp32."""
+    dev = x_in.device
+    L = len(weights)
+    if y_out is None:
+        y_out = torch.empty((chunk.total_tokens, cfg.d_model), dtype=torch.float32, device=dev)
+    c, ca, j = cfg.c(), cache.c(), chunk.c()
+    if workspace is None:
+        nbytes = lib().hstu_extend_workspace_bytes(ctypes.byref(c), ctypes.byref(ca), j.batch,
+                                                   j.total_tokens)
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    arr = (LayerWeightsT * L)(*[w.c() for w in weights])
+    _check(lib().hstu_extend(ctypes.byref(c), L, arr, ctypes.byref(ca), ctypes.byref(j),
+                             _p(seq_ids), max_context, window, sinks, _p(x_in), _p(y_out),
+                             _p(workspace), workspace.numel(), _stream(stream)), "hstu_extend")
+    return y_out
+
+
 def device_status(stream=None) -> int:
     """Synchronise, read and clear the library's device status word."""
     return lib().hstu_get_device_status(_stream(stream))
@@ -460,7 +657,7 @@ def profiler_start():
 
 def profiler_stop() -> dict:
     """Stop the profiler; returns {kernel name: (launches, total milliseconds)}."""
-    arr = (KernelTimeT * 16)()
+    arr = (KernelTimeT * 32)()
     n = ctypes.c_int32(0)
-    _check(lib().hstu_profiler_stop(arr, 16, ctypes.byref(n)), "hstu_profiler_stop")
+    _check(lib().hstu_profiler_stop(arr, 32, ctypes.byref(n)), "hstu_profiler_stop")
     return {arr[i].name.decode(): (arr[i].launches, arr[i].total_ms) for i in range(n.value)}

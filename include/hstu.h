@@ -352,6 +352,154 @@ hstu_status_t mfalcon_score(const hstu_layer_cfg_t* cfg, int32_t num_layers,
                             size_t ws_bytes, void* stream);
 
 /*
+ * ---- Paged history cache
+ *
+ * Keys, values and timestamps of many sequences (users, or branches of one) in
+ * fixed-size pages, so that histories grow, fork and shrink without moving.  The
+ * pages name "cacheable" operations (review section 三, M-FALCON) and no storage
+ * for them; this layout is the library's own.
+ *   kv          device [num_layers, num_pages, 2, num_heads, page_size, 64] in
+ *               `dtype` (K, then V, of every head): HSTU_FP16 for bf16 layers
+ *               (whose attention operands are fp16), HSTU_FP32 for fp32 layers,
+ *               any of the three for hstu_paged_attn_fwd alone
+ *   timestamps  device int64 [num_pages, page_size], one set for all layers
+ *   ref_count   device int32 [num_pages]: block-table entries that name the page;
+ *               0 = free.  A new cache starts with all zeros.
+ *   block_table device int32 [num_seqs, max_blocks]: page of events
+ *               b * page_size .. of a sequence, -1 = none.  Starts with all -1.
+ *   lengths     device int32 [num_seqs]: events per sequence.  Starts at 0.
+ * The caller owns the five arrays; they are the whole state (there is no free
+ * list: a free page is one whose count is 0, and the lowest ids are taken first).
+ * page_size is 16, 32, 64 or 128; num_pages * 2 * num_heads * page_size < 2^31 - 64.
+ *
+ * Calls that take `chunk` and `seq_ids`: chunk->offsets [batch + 1] are the row
+ * ranges of each sequence's new events (chunk->total_tokens rows in all, at most
+ * chunk->max_len per sequence, 0 allowed), chunk->timestamps their times;
+ * seq_ids device int32 [batch] names the sequences (NULL: 0 .. batch-1), each at
+ * most once.  After hstu_cache_reserve the chunk's rows are the last events of
+ * their sequences, and that is where append and attention find them.
+ *
+ * What the device finds wrong (a sequence out of range or named twice, a block
+ * table or pool that is too small, a page that is missing where a row sees it, a
+ * shared page that append would write) is reported as HSTU_ERR_DEVICE_CHECK in
+ * the device status word; nothing is read or written out of range.
+ */
+typedef struct {
+  int32_t num_layers;
+  int32_t num_heads;
+  int32_t dtype;              /* hstu_dtype_t of kv */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t num_seqs;
+  int32_t max_blocks;
+  void* kv;
+  int64_t* timestamps;
+  int32_t* ref_count;
+  int32_t* block_table;
+  int32_t* lengths;
+} hstu_cache_t;
+
+/* Workspace bytes of hstu_cache_reserve (for `batch` sequences) and of
+ * hstu_cache_compact; 0 for an invalid cache. */
+size_t hstu_cache_workspace_bytes(const hstu_cache_t* cache, int32_t batch);
+
+/* Makes room for the chunk's events and lengthens their sequences: takes free
+ * pages, replaces a partly filled last page that other sequences share by a copy
+ * of its filled rows (every layer), writes the events' timestamps, adds their
+ * counts to lengths.  All or nothing: when the pool or a block table is too
+ * small, or a sequence is named twice, HSTU_ERR_DEVICE_CHECK is recorded and
+ * nothing changes; read the status before appending if that can happen.
+ * Two launches. */
+hstu_status_t hstu_cache_reserve(const hstu_cache_t* cache, const hstu_jagged_t* chunk,
+                                 const int32_t* seq_ids, void* workspace, size_t ws_bytes,
+                                 void* stream);
+
+/* Writes K and V of the chunk's rows (the last events of their sequences) into
+ * one layer's pages.  k, v: device rows of num_heads * 64 elements of the cache's
+ * type, ldk and ldv elements apart, 16-byte aligned.  Pages that ref_count shows
+ * as shared are not written. */
+hstu_status_t hstu_cache_append(const hstu_cache_t* cache, int32_t layer,
+                                const hstu_jagged_t* chunk, const int32_t* seq_ids, const void* k,
+                                int64_t ldk, const void* v, int64_t ldv, void* stream);
+
+/* Copies whole sequences out of their pages into dense rows, all layers:
+ * offsets device int64 [batch + 1] (their differences are the sequences'
+ * lengths), total = offsets[batch], kv_out device [num_layers][total, 2,
+ * num_heads, 64] (the layout of hstu_forward's kv_cache_out, so mfalcon_score
+ * takes it), timestamps_out device int64 [total] or NULL.  A sequence may be
+ * named more than once. */
+hstu_status_t hstu_cache_gather(const hstu_cache_t* cache, int32_t batch, const int32_t* seq_ids,
+                                const int64_t* offsets, int64_t total, void* kv_out,
+                                int64_t* timestamps_out, void* stream);
+
+/* Forks count sequences: dst_ids[i] (an empty sequence) becomes a copy of
+ * src_ids[i] that shares its pages.  A source may be forked many times in one
+ * call; no destination may be named twice or be a source.  device int32 [count]. */
+hstu_status_t hstu_cache_fork(const hstu_cache_t* cache, int32_t count, const int32_t* src_ids,
+                              const int32_t* dst_ids, void* stream);
+
+/* Releases pages of count sequences (device int32 seq_ids[count]).  window == 0:
+ * all of them, and the sequence becomes empty.  window > 0: the blocks that no
+ * event after the last one can see through (window, sinks); the sequence keeps
+ * its length.  A sequence named twice is released once. */
+hstu_status_t hstu_cache_release(const hstu_cache_t* cache, int32_t count, const int32_t* seq_ids,
+                                 int32_t window, int32_t sinks, void* stream);
+
+/* Moves the used pages into the lowest ids (the k-th used page at or past the
+ * number of used pages goes to the k-th free page below it), every layer and the
+ * timestamps, and rewrites block_table and ref_count.  live_out device int32 [1]
+ * or NULL receives the number of used pages.  Two launches. */
+hstu_status_t hstu_cache_compact(const hstu_cache_t* cache, int32_t* live_out, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* Eq. 2 for the chunk's rows over the cache: row r of a sequence with n events
+ * and c new ones sits at position i = n - c + r and attends to every cached event
+ * j <= i (itself included; reserve and append come first):
+ *   AV_i = sum_j phi2(q_i.k_j + rab_pos[h, min(i-j, P-1)] + rab_time[h, bt(t_i - t_j)]) v_j / n
+ * (softmax over the visible keys for HSTU_ACT_SOFTMAX), the last c rows of
+ * hstu_attn_fwd over the whole sequence.
+ *   cfg         dtype = cache->dtype, num_heads = cache->num_heads
+ *   window      0, or W > 0: a row sees only j > i - W and the first `sinks` events;
+ *               events that no row of the chunk sees may have no page.  N stays n.
+ *   max_context >= every length (the launch is sized from it)
+ *   q           device rows of H*64, ldq elements apart, 16-byte aligned
+ *   av_out      device [T, H*64] in cfg->dtype (fp32 in the _f32 form)
+ * Any sequence length that the block table holds.  Values of V that some row of the chunk
+ * sees must be finite (a product with a masked weight is still formed);
+ * everything else, unwritten slots of a page included, may hold anything.  A
+ * visible event 2^31 - 3 seconds or more before the last one is reported.  One launch;
+ * needs no workspace; bit-reproducible. */
+hstu_status_t hstu_paged_attn_fwd(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                  int32_t layer, const hstu_jagged_t* chunk,
+                                  const int32_t* seq_ids, int32_t max_context, int32_t window,
+                                  int32_t sinks, const void* q, int64_t ldq, const float* rab_pos,
+                                  const float* rab_time, void* av_out, void* stream);
+hstu_status_t hstu_paged_attn_fwd_f32(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                      int32_t layer, const hstu_jagged_t* chunk,
+                                      const int32_t* seq_ids, int32_t max_context, int32_t window,
+                                      int32_t sinks, const void* q, int64_t ldq,
+                                      const float* rab_pos, const float* rab_time, float* av_out,
+                                      void* stream);
+
+/* Workspace bytes of hstu_extend for `total_tokens` new events of `batch` sequences. */
+size_t hstu_extend_workspace_bytes(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
+                                   int32_t batch, int64_t total_tokens);
+
+/* Runs new events through the stack against the cache: reserves their pages, then
+ * for every layer f1, append, hstu_paged_attn_fwd and f2.  The results are those
+ * of hstu_forward's rows for the same events, except that earlier events keep
+ * the keys and values of the calls that brought them (whose N was the length then;
+ * Norm removes that scale up to ln_eps).
+ *   cache        num_layers = the stack's; dtype fp16 for bf16 layers, fp32 for fp32
+ *   x_in         device [T, d] in cfg dtype, y_out device [T, d] fp32
+ * When the reservation fails the cache is unchanged and y_out is unspecified. */
+hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
+                          const hstu_layer_weights_t* weights, const hstu_cache_t* cache,
+                          const hstu_jagged_t* chunk, const int32_t* seq_ids, int32_t max_context,
+                          int32_t window, int32_t sinks, const void* x_in, float* y_out,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Stochastic Length (review section 三, Stochastic Length): every user's n
  * events are shortened to L = min(n, ceil(n u^(1/alpha))), u ~ Uniform(0, 1],
  * keeping a uniformly random subset of L events in time order.

@@ -1,0 +1,523 @@
+"""The paged history cache on the GPU against its float64 oracle (oracle/paged.py)."""
+import numpy as np
+import pytest
+import torch
+
+from gen import make_case
+from gen.device import case_tensors, tensor
+from gen.inputs import make_attn_case
+from oracle import hstu as O
+from oracle import paged as P
+from hstu_testutil import assert_close, binding, config_of
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8, "fp32": 2.0 ** -24}  # half a step, relative
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def H():
+    return binding()
+
+
+def i32(a):
+    return torch.tensor(list(a), dtype=torch.int32, device="cuda")
+
+
+def chunk_of(H, counts, ts):
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    return H.Jagged(tensor(off, torch.int64, "cuda"), tensor(np.asarray(ts, dtype=np.int64), torch.int64, "cuda"),
+                    int(max(counts, default=0)), int(off[-1]))
+
+
+def nan_cache(H, *, layers, heads, pages, seqs, blocks, ps, dtype):
+    """An empty cache whose every slot holds NaN, and times that no event has."""
+    c = H.PagedCache.empty(layers, heads, pages, seqs, blocks, ps, dtype)
+    c.kv.fill_(float("nan"))
+    c.timestamps.fill_(-(1 << 62))
+    return c
+
+
+def split_rows(offsets, counts, tail):
+    """Row indices of each sequence's first n - c events (tail False) or last c."""
+    idx = []
+    for u, c in enumerate(counts):
+        a, b = int(offsets[u]), int(offsets[u + 1])
+        idx.append(np.arange(b - c, b) if tail else np.arange(a, b - c))
+    return np.concatenate(idx) if idx else np.zeros(0, dtype=np.int64)
+
+
+def load_cache(H, ac, cache, counts, layer=0, seq_ids=None):
+    """Reserve and append all but the last counts[u] events, then those; returns the chunk."""
+    lens = np.diff(ac.offsets)
+    dt = cache.kv.dtype
+    for tail in (False, True):
+        rows = split_rows(ac.offsets, counts, tail)
+        j = chunk_of(H, counts if tail else [int(n - c) for n, c in zip(lens, counts)], ac.timestamps[rows])
+        H.cache_reserve(cache, j, seq_ids=seq_ids)
+        # K and V as column blocks of one buffer
+        kv = torch.cat([tensor(ac.v[rows], dt, "cuda"), tensor(ac.k[rows], dt, "cuda")], 1)
+        hv = ac.k.shape[1]
+        H.cache_append(cache, layer, j, kv[:, hv:], kv[:, :hv], seq_ids=seq_ids)
+    return j, rows
+
+
+def attn_bound(q, k, v, s, a, vis, n, phi2, dtype, out16):
+    """Element-wise bound of the kernel's error for one head, from the roundings
+    it makes: S in fp32 (64-term dot: 64 * 2^-24 of sum |q k|, and the sums of S with
+    its biases), phi2 (SiLU: h + h tanh(h), the hardware tanh within 2^-11 relative;
+    2^x within 2^-22), P rounded to the operand type, fp32 accumulation over the
+    keys, and the output's own rounding."""
+    u = UNIT[dtype] if dtype != "fp32" else 0.0
+    ds = 2.0 ** -17 * (np.abs(q) @ np.abs(k).T) + 2.0 ** -22 * np.abs(s)
+    if phi2 == "softmax":
+        # numerator and denominator each move by exp's relative error ds + 2^-22; P's
+        # rounding, and below 2^-14 fp16's fixed step 2^-25 relative to the largest weight
+        rel = 2.0 * (ds + 2.0 ** -21).max(axis=1, keepdims=True, where=vis, initial=0.0) + u
+        err = a * rel + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    else:
+        p = np.abs(a) * n
+        act = 2.0 ** -11 * np.abs(s) / 2 if phi2 == "silu" and dtype != "fp32" else 2.0 ** -21 * p
+        err = (1.2 * ds + act + u * p + (2.0 ** -25 if dtype == "fp16" else 0.0)) / n
+    err = np.where(vis, err, 0.0)
+    e = err @ np.abs(v) + 2.0 ** -24 * (8 + a.shape[1] / 16) * (np.abs(a) @ np.abs(v))
+    # the output's rounding: half a step is out16 relative, and below fp16's least normal
+    # number 2^-14, where the steps stay 2^-24 wide, 2^-25 absolute
+    least = 2.0 ** -25 if dtype == "fp16" and out16 else 1e-30
+    return 1.01 * e + np.maximum(out16 * np.abs(a @ v), least)
+
+
+LENS = [(1, 1), (5, 5), (64, 1), (65, 1), (130, 2), (300, 17), (0, 0), (257, 40), (50, 0), (1000, 33), (128, 128)]
+
+
+def run_attn(H, lens, heads, dtype, phi2, ps, window=0, sinks=0, Pb=64, Tb=64, gap="exp", seed=7, f32=False,
+             release=False, spread=None):
+    counts = [c for _, c in lens]
+    ac = make_attn_case([n for n, _ in lens], heads, Pb, Tb, seed=seed, dtype=dtype, gap_kind=gap)
+    total = sum(-(-n // ps) for n, _ in lens)
+    blocks = max(-(-n // ps) for n, _ in lens) + 1
+    cache = nan_cache(H, layers=2, heads=heads, pages=total + 5, seqs=len(lens) + 2, blocks=blocks, ps=ps, dtype=dtype)
+    perm = np.random.default_rng(seed).permutation(len(lens) + 2)[:len(lens)]
+    seq = i32(perm)
+    j, rows = load_cache(H, ac, cache, counts, layer=1, seq_ids=seq)
+    if release:  # what a row at n or later does not see; rows of this chunk may see a little more
+        keep = window + max(counts)
+        H.cache_release(cache, seq, window=keep, sinks=sinks)
+    cfg = H.LayerConfig(64 * heads, heads, Pb, Tb, phi2=phi2, dtype=dtype)
+    q = tensor(ac.q[rows], DT[dtype], "cuda")
+    fn = H.paged_attn_fwd_f32 if f32 else H.paged_attn_fwd
+    rp, rt = tensor(ac.rab_pos, torch.float32, "cuda"), tensor(ac.rab_time, torch.float32, "cuda")
+    wide = torch.cat([torch.full_like(q, float("nan")), q], 1)  # a row stride, NaN beside the rows
+    args = (cfg, cache, 1, j, wide[:, heads * 64:], rp, rt, max(n for n, _ in lens))
+    got = fn(*args, window=window, sinks=sinks, seq_ids=seq)
+    again = fn(*args, window=window, sinks=sinks, seq_ids=seq)
+    assert H.device_status() == 0
+    assert torch.equal(got, again)  # the same bits
+    got = got.float().cpu().numpy().astype(np.float64)
+    at = 0
+    for u, (n, c) in enumerate(lens):
+        if c == 0:
+            continue
+        s = slice(int(ac.offsets[u]), int(ac.offsets[u + 1]))
+        k, v, ts = ac.k[s].astype(np.float64), ac.v[s].astype(np.float64), ac.timestamps[s]
+        qu = ac.q[s][n - c:].astype(np.float64)
+        want, ss, aa = P.chunk_attention(qu, k, v, ts, ac.rab_pos.astype(np.float64),
+                                         ac.rab_time.astype(np.float64), heads, phi2, window, sinks, parts=True)
+        for h in range(heads):
+            cols = slice(h * 64, h * 64 + 64)
+            tol = attn_bound(qu[:, cols], k[:, cols], v[:, cols], ss[h], aa[h],
+                             P.window_mask(n, c, window, sinks), n, phi2, dtype,
+                             0.0 if f32 else UNIT[dtype])
+            err = np.abs(got[at:at + c, cols] - want[:, cols])
+            worst = np.nanmax(err / tol) if np.isfinite(err).all() else np.inf
+            assert worst <= 1.0, (u, n, c, h, worst, err.max())
+        at += c
+    return cache
+
+
+@pytest.mark.parametrize("ps", [16, 32, 64, 128])
+@pytest.mark.parametrize("phi2", ["silu", "softmax"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_attention(H, dtype, phi2, ps):
+    run_attn(H, LENS, 3, dtype, phi2, ps)
+
+
+@pytest.mark.parametrize("phi2", ["relu", "identity"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
+def test_attention_other_phi(H, dtype, phi2):
+    run_attn(H, LENS, 1, dtype, phi2, 32, gap="lognormal", Pb=1024, Tb=128)
+
+
+@pytest.mark.parametrize("dtype,phi2", [("fp16", "silu"), ("bf16", "softmax"), ("fp32", "silu"), ("fp32", "softmax")])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (64, 0), (100, 70), (63, 200), (5000, 10)])
+def test_attention_window(H, dtype, phi2, window, sinks):
+    run_attn(H, LENS, 2, dtype, phi2, 16, window=window, sinks=sinks, Pb=512)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(30, 0), (30, 20), (100, 130)])
+def test_attention_over_released_pages(H, dtype, window, sinks):
+    """Pages that fell out of the window are gone; the rows read none of them."""
+    lens = [(400, 3), (1000, 20), (77, 1), (640, 30), (129, 129)]
+    cache = run_attn(H, lens, 2, dtype, "silu", 16, window=window, sinks=sinks, Pb=512, release=True)
+    assert int((cache.block_table[:, :20] < 0).sum()) > 20
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_attention_f32_output(H, dtype):
+    run_attn(H, [(300, 17), (90, 90), (1, 1)], 2, dtype, "silu", 64, f32=True)
+
+
+def test_attention_one_row_of_many_lengths(H):
+    """Single events over lengths around tile and split borders, in a batch and alone."""
+    lens = [(n, 1) for n in (1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 511, 512, 513, 2000)]
+    run_attn(H, lens, 2, "fp16", "silu", 64)
+    for n in (1, 64, 1025, 4100):
+        run_attn(H, [(n, 1)], 1, "fp16", "softmax", 16, Pb=4096)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("phi2", ["silu", "softmax"])
+def test_attention_long_chunks(H, dtype, phi2):
+    run_attn(H, [(700, 700), (1300, 300), (400, 1), (600, 257), (520, 65)], 2, dtype, phi2, 64, Pb=600)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (50, 10), (300, 129), (128, 64)])
+def test_attention_long_chunks_window(H, dtype, window, sinks):
+    run_attn(H, [(1500, 600), (1300, 300), (400, 1), (257, 257)], 1, dtype, "silu", 32, window=window,
+             sinks=sinks, Pb=2048, gap="lognormal")
+
+
+def test_far_offsets_in_a_large_cache(H):
+    """Page addresses past 2^32 bytes (a cache of 5 GB)."""
+    heads, ps = 4, 64
+    pages = (5 << 30) // (2 * heads * ps * 64 * 2)
+    cache = H.PagedCache.empty(1, heads, pages, 1, 8, ps, "fp16")
+    cache.ref_count.fill_(1)
+    cache.ref_count[-8:] = 0
+    ac = make_attn_case([200], heads, 64, 64, seed=3, dtype="fp16")
+    j, rows = load_cache(H, ac, cache, [9])
+    assert int(cache.block_table[0, 0]) == pages - 8
+    cfg = H.LayerConfig(64 * heads, heads, 64, 64, dtype="fp16")
+    got = H.paged_attn_fwd_f32(cfg, cache, 0, j, tensor(ac.q[rows], torch.float16, "cuda"),
+                               tensor(ac.rab_pos, torch.float32, "cuda"),
+                               tensor(ac.rab_time, torch.float32, "cuda"), 200)
+    kv, ts = H.cache_gather(cache, tensor(np.array([0, 200]), torch.int64, "cuda"), 200)
+    assert H.device_status() == 0
+    assert np.array_equal(kv[0, :, :256].float().cpu().numpy(), ac.k)
+    assert np.array_equal(ts.cpu().numpy(), ac.timestamps)
+    f = np.float64
+    want = P.chunk_attention(ac.q[191:].astype(f), ac.k.astype(f), ac.v.astype(f), ac.timestamps,
+                             ac.rab_pos.astype(f), ac.rab_time.astype(f), heads)
+    assert_close(got.cpu().numpy(), want, "attention in a 5 GB cache")
+
+
+# ---------------------------------------------------------------- rows and pages
+
+def tables(cache):
+    return cache.block_table.tolist(), cache.lengths.tolist(), cache.ref_count.tolist()
+
+
+def same_pages(cache, pg):
+    t, n, r = tables(cache)
+    assert n == pg.len and r == pg.ref
+    for row, want, ln in zip(t, pg.table, pg.len):
+        assert row[:pg.blocks(ln)] == want[:pg.blocks(ln)]
+
+
+@pytest.mark.parametrize("ps", [16, 128])
+def test_pages_follow_the_oracle(H, ps):
+    """A random life of a cache: every table, length and count equal after every
+    call, and every event's rows and time found where the tables say, in all layers."""
+    rng = np.random.default_rng(ps)
+    heads, layers, seqs, blocks, pages = 2, 3, 7, 6, 25
+    cache = nan_cache(H, layers=layers, heads=heads, pages=pages, seqs=seqs, blocks=blocks, ps=ps, dtype="fp16")
+    pg = P.Pages(pages, seqs, blocks, ps)
+    hold = [[] for _ in range(seqs)]  # (serial, time) of each sequence's events
+    gone = [set() for _ in range(seqs)]
+    serial = refused = 0
+
+    def rows(ids, layer, which):
+        x = np.asarray(ids, dtype=np.int64)[:, None] * 7 + 3 * layer + which + np.arange(heads * 64)[None, :]
+        return (x % 1999).astype(np.float32)
+
+    for step in range(120):
+        op = rng.choice(["reserve", "reserve", "reserve", "fork", "release", "trim", "compact"])
+        if op == "reserve":
+            b = int(rng.integers(1, seqs + 1))
+            ids = rng.permutation(seqs)[:b].tolist()
+            cnt = [int(x) for x in rng.integers(0, 2 * ps, b)]
+            new = [list(range(serial + sum(cnt[:i]), serial + sum(cnt[:i + 1]))) for i in range(b)]
+            flat = [x for r in new for x in r]
+            j = chunk_of(H, cnt, [10 * x + 1 for x in flat])
+            ok = pg.reserve(ids, cnt) is not None
+            H.cache_reserve(cache, j, seq_ids=i32(ids))
+            assert H.device_status() == (0 if ok else 6)
+            refused += not ok
+            if ok and flat:
+                serial += len(flat)
+                for s, r in zip(ids, new):
+                    hold[s] += r
+                for l in range(layers):
+                    H.cache_append(cache, l, j, tensor(rows(flat, l, 0), torch.float16, "cuda"),
+                                   tensor(rows(flat, l, 1), torch.float16, "cuda"), seq_ids=i32(ids))
+        elif op == "fork":
+            full = [s for s in range(seqs) if pg.len[s]]
+            empty = [s for s in range(seqs) if not pg.len[s]]
+            if not full or not empty:
+                continue
+            src = [int(rng.choice(full)) for _ in empty]
+            H.cache_fork(cache, i32(src), i32(empty))
+            for a, d in zip(src, empty):
+                pg.fork(a, d)
+                hold[d], gone[d] = list(hold[a]), set(gone[a])
+        elif op == "release":
+            ids = [int(x) for x in rng.integers(0, seqs, 2)]
+            H.cache_release(cache, i32(ids + ids[:1]))  # named twice: released once
+            for s in set(ids):
+                pg.release(s)
+                hold[s], gone[s] = [], set()
+        elif op == "trim":
+            s, w, k = int(rng.integers(seqs)), int(rng.integers(1, 3 * ps)), int(rng.integers(0, 2 * ps))
+            H.cache_release(cache, i32([s]), window=w, sinks=k)
+            pg.release(s, w, k)
+        else:
+            live = H.cache_compact(cache)
+            pg.compact()
+            assert int(live) == sum(r > 0 for r in pg.ref)
+        assert H.device_status() == 0
+        same_pages(cache, pg)
+        kv, ts = cache.kv.float().cpu().numpy(), cache.timestamps.cpu().numpy()
+        for s in range(seqs):
+            for b in range(pg.blocks(pg.len[s])):
+                page = pg.table[s][b]
+                if page < 0:
+                    continue
+                ids = hold[s][b * ps:(b + 1) * ps]
+                m = len(ids)
+                assert ts[page, :m].tolist() == [10 * x + 1 for x in ids]
+                for l in range(layers):
+                    for which in (0, 1):
+                        got = kv[l, page, which, :, :m].transpose(1, 0, 2).reshape(m, heads * 64)
+                        assert np.array_equal(got, rows(ids, l, which)), (step, op, s, b, l, which)
+    assert refused > 0  # the pool ran out at least once, and nothing changed then
+
+
+def test_gather_whole_sequences(H):
+    lens = [0, 1, 100, 33, 257]
+    for dtype in ("fp16", "bf16", "fp32"):
+        ac = make_attn_case(lens, 3, 16, 16, seed=4, dtype=dtype)
+        cache = nan_cache(H, layers=2, heads=3, pages=40, seqs=6, blocks=18, ps=16, dtype=dtype)
+        for l in range(2):
+            if l == 0:
+                load_cache(H, ac, cache, [n // 2 for n in lens])
+            else:
+                j = chunk_of(H, lens, ac.timestamps)
+                H.cache_append(cache, 1, j, tensor(ac.v, DT[dtype], "cuda"), tensor(ac.k, DT[dtype], "cuda"))
+        ids = [4, 1, 4, 0, 2]
+        off = np.concatenate([[0], np.cumsum([lens[i] for i in ids])]).astype(np.int64)
+        kv, ts = H.cache_gather(cache, tensor(off, torch.int64, "cuda"), int(off[-1]), seq_ids=i32(ids))
+        assert H.device_status() == 0
+        rows = np.concatenate([np.arange(ac.offsets[i], ac.offsets[i + 1]) for i in ids])
+        assert np.array_equal(ts.cpu().numpy(), ac.timestamps[rows])
+        kv = kv.float().cpu().numpy()
+        assert np.array_equal(kv[0], np.concatenate([ac.k[rows], ac.v[rows]], 1))
+        assert np.array_equal(kv[1], np.concatenate([ac.v[rows], ac.k[rows]], 1))
+
+
+def test_reports_instead_of_writing(H):
+    """Wrong sequences, missing pages, shared pages and wrong lengths are reported
+    and leave everything as it was."""
+    ac = make_attn_case([40, 20], 1, 16, 16, seed=5, dtype="fp16")
+    cache = nan_cache(H, layers=1, heads=1, pages=12, seqs=4, blocks=4, ps=16, dtype="fp16")
+    j, rows = load_cache(H, ac, cache, [3, 2])
+    x = tensor(ac.k[rows], torch.float16, "cuda")
+
+    def unchanged(call):
+        before = [t.clone() for t in (cache.kv, cache.timestamps, *map(torch.tensor, tables(cache)))]
+        call()
+        assert H.device_status() == 6
+        after = (cache.kv, cache.timestamps, *map(torch.tensor, tables(cache)))
+        for a, b in zip(before, after):
+            assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+    for ids in ([1, 1], [0, 4], [-1, 0]):  # twice, past the end, negative
+        unchanged(lambda: H.cache_reserve(cache, j, seq_ids=i32(ids)))
+    unchanged(lambda: H.cache_reserve(cache, chunk_of(H, [30, 1], [0] * 31)))     # block table too short
+    unchanged(lambda: H.cache_append(cache, 0, j, x, x, seq_ids=i32([-1, 9])))
+    unchanged(lambda: H.cache_append(cache, 0, chunk_of(H, [0, 21], [0] * 21),
+                                     x[:1].expand(21, 64).contiguous(), x[:1].expand(21, 64).contiguous()))
+    unchanged(lambda: H.cache_fork(cache, i32([0]), i32([1])))                       # not empty
+    unchanged(lambda: H.cache_fork(cache, i32([0]), i32([0])))
+    unchanged(lambda: H.cache_fork(cache, i32([7]), i32([2])))
+    unchanged(lambda: H.cache_release(cache, i32([17])))
+    # a fork shares its pages: they are not written
+    H.cache_fork(cache, i32([0]), i32([2]))
+    assert H.device_status() == 0
+    unchanged(lambda: H.cache_append(cache, 0, chunk_of(H, [3], [0] * 3), x[:3], x[:3]))
+    # attention: a visible page that is missing, a context longer than declared
+    cfg = H.LayerConfig(64, 1, 16, 16, dtype="fp16")
+    rp = torch.zeros((1, 16), device="cuda")
+
+    def attn(ctx=40, **kw):
+        return H.paged_attn_fwd(cfg, cache, 0, j, x, rp, rp, ctx, **kw)
+
+    attn()
+    assert H.device_status() == 0
+    unchanged(lambda: attn(ctx=39))
+    unchanged(lambda: attn(seq_ids=i32([0, 4])))
+    page = int(cache.block_table[0, 0])
+    for bad in (-1, 12, 1 << 30):
+        cache.block_table[0, 0] = bad
+        unchanged(attn)
+        attn(window=8)  # out of the window: not looked at
+        assert H.device_status() == 0
+    cache.block_table[0, 0] = page
+
+
+def test_reserve_many_sequences(H):
+    """More sequences than one pass of the bookkeeping kernel takes (1024), in a
+    pool larger than one scan (4096 pages)."""
+    n = 2500
+    cache = H.PagedCache.empty(1, 1, 9000, n, 5, 16, "fp16")
+    pg = P.Pages(9000, n, 5, 16)
+    rng = np.random.default_rng(1)
+    for _ in range(2):
+        cnt = [int(x) for x in rng.integers(0, 40, n)]
+        H.cache_reserve(cache, chunk_of(H, cnt, range(sum(cnt))))
+        pg.reserve(list(range(n)), cnt)
+        assert H.device_status() == 0
+        same_pages(cache, pg)
+    gone = [int(x) for x in rng.permutation(n)[:1200]]
+    H.cache_release(cache, i32(gone))
+    for s in gone:
+        pg.release(s)
+    H.cache_compact(cache)
+    pg.compact()
+    same_pages(cache, pg)
+
+
+# ---------------------------------------------------------------- together
+
+@pytest.mark.parametrize("name,kw", [("tiny-fp32", {}), ("small-bf16", {}), ("small-bf16", dict(window=40, sinks=9)),
+                                     ("small-bf16", dict(phi2="softmax"))])
+def test_extend_follows_the_oracle(H, name, kw):
+    """Histories in several requests through a stack, against the incremental oracle."""
+    kw = dict(kw)
+    phi2 = kw.pop("phi2", "silu")
+    lens = [130, 64, 1, 47]
+    case = make_case(make_case(name).cfg.replace(phi2=phi2, num_layers=2), seed=11, lengths=lens)
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    cache = nan_cache(H, layers=2, heads=case.cfg.num_heads, pages=40, seqs=4, blocks=9, ps=16,
+                      dtype="fp32" if name == "tiny-fp32" else "fp16")
+    cuts = [[0, 100, 101, 130], [0, 10, 63, 64], [0, 0, 1, 1], [0, 30, 30, 47]]
+    state = [None] * 4
+    for step in range(3):
+        rows = np.concatenate([case.offsets[u] + np.arange(cuts[u][step], cuts[u][step + 1]) for u in range(4)])
+        cnt = [cuts[u][step + 1] - cuts[u][step] for u in range(4)]
+        j = chunk_of(H, cnt, case.timestamps[rows])
+        y = H.extend(cfg, weights, cache, j, t["x"][torch.from_numpy(rows).cuda()].contiguous(), 130, **kw)
+        if kw:
+            H.cache_release(cache, i32(range(4)), **kw)
+        assert H.device_status() == 0
+        want = []
+        for u in range(4):
+            a, b = case.offsets[u] + cuts[u][step], case.offsets[u] + cuts[u][step + 1]
+            if b > a:
+                w, state[u] = P.extend(state[u], case.x[a:b], case.timestamps[a:b], case.layers, case.cfg, **kw)
+                want.append(w)
+        assert_close(y.cpu().numpy(), np.concatenate(want), f"extend {name} {phi2} {kw} step {step}")
+
+
+def test_serving_round(H):
+    """A request as a server makes it: encode a history, keep it in pages, branch
+    it, extend the branches, score candidates over one of them; every part
+    against the same through the dense calls."""
+    case = make_case(make_case("mfalcon").cfg.replace(num_layers=2, num_cand=24, d_model=256, num_heads=4),
+                     seed=12, lengths=[120, 75])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    jag = H.Jagged(t["offsets"], t["timestamps"], case.max_len, case.total_tokens)
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    hv = 256
+    dense = torch.empty((2, case.total_tokens, 2 * hv), dtype=torch.float16, device="cuda")
+    H.forward(cfg, weights, jag, t["x"], kv_cache_out=dense)
+    cache = nan_cache(H, layers=2, heads=4, pages=30, seqs=6, blocks=12, ps=16, dtype="fp16")
+    H.cache_reserve(cache, jag)
+    for l in range(2):
+        H.cache_append(cache, l, jag, dense[l, :, :hv], dense[l, :, hv:])
+    kv, ts = H.cache_gather(cache, t["offsets"], case.total_tokens)
+    assert torch.equal(kv, dense) and torch.equal(ts, t["timestamps"])
+    args = (t["cand_offsets"], t["cand_emb"], t["request_ts"], 8, 24)
+    assert torch.equal(H.mfalcon_score(cfg, weights, jag, kv, *args), H.mfalcon_score(cfg, weights, jag, dense, *args))
+    # two branches of user 0: the same events give the same rows, other events leave them alone
+    H.cache_fork(cache, i32([0, 0]), i32([2, 3]))
+    x_new = t["x"][:6].contiguous()
+    last = int(case.timestamps[119])
+    j = chunk_of(H, [3, 3], [last + 1 + i for i in range(3)] * 2)
+    y = H.extend(cfg, weights, cache, j, torch.cat([x_new[:3], x_new[:3]]), 200, seq_ids=i32([2, 3]))
+    assert H.device_status() == 0
+    assert torch.equal(y[:3], y[3:])
+    kv2, _ = H.cache_gather(cache, t["offsets"], case.total_tokens)
+    assert torch.equal(kv2, dense)  # the parent is as it was
+    H.cache_release(cache, i32([2, 3]))
+    H.cache_compact(cache)
+    kv2, _ = H.cache_gather(cache, t["offsets"], case.total_tokens)
+    assert torch.equal(kv2, dense) and H.device_status() == 0
+    # the same extension without the branch, and against the incremental oracle's dense rows
+    y2 = H.extend(cfg, weights, cache, chunk_of(H, [3], [last + 1 + i for i in range(3)]), x_new[:3], 200,
+                  seq_ids=i32([0]))
+    assert_close(y2.cpu().numpy(), y[:3].cpu().numpy(), "extension of a user and of its branch")
+
+
+def test_refused_extension_leaves_the_cache(H):
+    case = make_case("small-bf16", seed=13, lengths=[60])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    cache = nan_cache(H, layers=case.cfg.num_layers, heads=case.cfg.num_heads, pages=4, seqs=1, blocks=9, ps=16,
+                      dtype="fp16")
+    H.extend(cfg, weights, cache, chunk_of(H, [50], case.timestamps[:50]), t["x"][:50], 60)
+    assert H.device_status() == 0
+    kv, ts = cache.kv.clone(), cache.timestamps.clone()
+    H.extend(cfg, weights, cache, chunk_of(H, [60], range(60)), t["x"], 200)
+    assert H.device_status() == 6
+    assert torch.equal(torch.nan_to_num(kv), torch.nan_to_num(cache.kv)) and torch.equal(ts, cache.timestamps)
+    assert cache.lengths.tolist() == [50]
+
+
+def test_captured_and_on_another_stream(H):
+    """Two graphs with their own workspaces, replayed in turn on a side stream."""
+    ac = make_attn_case([300, 200], 2, 64, 64, seed=8, dtype="fp16")
+    cache = nan_cache(H, layers=1, heads=2, pages=40, seqs=2, blocks=24, ps=16, dtype="fp16")
+    j, rows = load_cache(H, ac, cache, [5, 70])
+    cfg = H.LayerConfig(128, 2, 64, 64, dtype="fp16")
+    rp, rt = tensor(ac.rab_pos, torch.float32, "cuda"), tensor(ac.rab_time, torch.float32, "cuda")
+    q = tensor(ac.q[rows], torch.float16, "cuda")
+    k, v = tensor(ac.k[rows], torch.float16, "cuda"), tensor(ac.v[rows], torch.float16, "cuda")
+    want = H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, 300)
+    want_w = H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, 300, window=20, sinks=3)
+    out, out_w = torch.zeros_like(want), torch.zeros_like(want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graphs = []
+    for o, kw in ((out, {}), (out_w, dict(window=20, sinks=3))):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            H.cache_append(cache, 0, j, k, v)
+            H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, 300, av_out=o, **kw)
+        graphs.append(g)
+    for _ in range(3):
+        out.zero_()
+        out_w.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for g in graphs:
+                g.replay()
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(out, want) and torch.equal(out_w, want_w)
+    assert H.device_status() == 0
