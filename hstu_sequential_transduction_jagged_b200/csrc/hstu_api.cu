@@ -103,6 +103,17 @@ const int64_t* thresholds_for(int Tb) {
   return table[Tb];
 }
 
+// The octave table of a bucket count, computed once; nullptr where it does not fit.
+const int4* octaves_for(int Tb) {
+  static std::mutex mu;
+  static int4 table[MAX_TIME_BUCKETS + 1][32];
+  static signed char ready[MAX_TIME_BUCKETS + 1] = {};
+  const int64_t* thr = thresholds_for(Tb);
+  std::lock_guard<std::mutex> lock(mu);
+  if (ready[Tb] == 0) ready[Tb] = compute_octaves(Tb, thr, table[Tb]) ? 1 : -1;
+  return ready[Tb] > 0 ? table[Tb] : nullptr;
+}
+
 // ------------------------------------------------------------------ profiler
 
 enum KernelKind : int {
@@ -1066,7 +1077,9 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int64_t* thr = thresholds_for(c->num_time_buckets);
   for (int b = 0; b < c->num_time_buckets; ++b)
     p.thr[b] = thr[b] < static_cast<int64_t>(INT32_MAX) ? static_cast<int32_t>(thr[b]) : INT32_MAX;
-  if (!compute_octaves(c->num_time_buckets, thr, p.oct)) return HSTU_ERR_UNSUPPORTED;
+  const int4* oct = octaves_for(c->num_time_buckets);
+  if (oct == nullptr) return HSTU_ERR_UNSUPPORTED;
+  std::memcpy(p.oct, oct, sizeof(p.oct));
   const int max_new = std::min(p.max_new, p.max_context);
   if (max_new == 0) return HSTU_OK;
   // the longest visible part of a context, in key tiles

@@ -53,6 +53,8 @@ struct PagedParams {
 
 constexpr int PG_KEYS = 64;  // keys per tile
 
+__device__ __forceinline__ int log2_small(int v) { return 31 - __clz(v); }
+
 // One sequence's part of a launch, the same for every CTA of its clusters.
 struct PagedSeq {
   int seq, n, c;       // table row, events, new events
@@ -278,8 +280,8 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 // 16 w .. 16 w + 15 of every 64-key tile for all the rows: S = Q K^T, the element
 // work and O += P V need no exchange between warps until the end.  A fifth warp
 // streams K, V (TMA, one box per page part, 128B swizzle), key times and the
-// position band through a ring of stages; table entries are read two tiles ahead
-// and times one tile ahead, so their latency stays off the ring.
+// position band (cp.async) through a ring of stages, and never waits for a value it
+// loads: block-table entries come 32 boxes at a time, a batch ahead.
 constexpr int PGS_WARPS = 4;
 constexpr int PGS_THREADS = (PGS_WARPS + 1) * 32;
 constexpr int PGS_STAGES = 4;
@@ -290,7 +292,7 @@ struct PgsSmem {
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kV = kK + PGS_STAGES * PGS_TILE_BYTES;
   static constexpr uint32_t kSide = kV + PGS_STAGES * PGS_TILE_BYTES;  // per stage: 64 times, 96 biases
-  static constexpr uint32_t kSideBytes = 64 * 4 + 96 * 4;
+  static constexpr uint32_t kSideBytes = 64 * 8 + 96 * 4;
   static constexpr uint32_t kTime = kSide + PGS_STAGES * kSideBytes;
   static constexpr uint32_t kThr = kTime + MAX_TIME_BUCKETS * 4;
   static constexpr uint32_t kOct = kThr + MAX_TIME_BUCKETS * 4;
@@ -302,6 +304,19 @@ struct PgsSmem {
   static constexpr uint32_t kBytes = kAbort + 16 + 1024;           // + align slack
   static_assert(PGS_WARPS * 32 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
 };
+
+// Asynchronous copies of 8 and 4 bytes; with `bytes` 0 the destination is zeroed.
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One arrival on the barrier (counted in its expected arrivals) when this
+// thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -403,7 +418,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   float2* sMlC = reinterpret_cast<float2*>(smem + PgsSmem::kMlC);
   if (tid == 0) {
     for (int k = 0; k < PGS_STAGES; ++k) {
-      mbar_init(&bar_full[k], 2);
+      mbar_init(&bar_full[k], 1 + 32);  // the expect-tx arrival, the producer lanes' copies
       mbar_init(&bar_empty[k], PGS_WARPS);
     }
     *sAbort = 0;
@@ -432,98 +447,68 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     const int psl = p.ps_log2, ps = 1 << psl;
     const int box = min(ps, PG_KEYS), nbox = PG_KEYS / box;
     const int32_t oob = static_cast<int32_t>((static_cast<int64_t>(p.num_pages) * 2 * p.H) << psl);
-    constexpr int NB = kBand / 32 + (kBand % 32 != 0);
-    // page of the lane's positions j0 + lane and j0 + 32 + lane, -1 where no row
-    // sees the position; a visible position without a page is reported
-    auto load_pages = [&](int kk, int (&pg)[2]) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        pg[e] = -1;
-        if (kk < k_end) {
-          const int j = s.tile(kk) * PG_KEYS + lane + 32 * e;
-          if (s.seen(j)) pg[e] = tab[j >> psl];
+    const int nbl = log2_small(nbox), per = 32 >> nbl;  // tiles per batch of block-table entries
+    const uint32_t sbase = smem_u32(smem);
+    // the page of box (lane % nbox) of tile k0 + lane / nbox; -1 where no row sees
+    // it (its rows are read as zeros), and where a page is missing, which is reported
+    auto load_pages = [&](int k0) -> int {
+      const int kk = k0 + (lane >> nbl);
+      if (kk >= k_end) return -1;
+      const int jb = s.tile(kk) * PG_KEYS + (lane & (nbox - 1)) * box;
+      if (jb >= s.n || (jb >= s.sink_end && jb + box <= s.lo)) return -1;
+      return tab[jb >> psl];
+    };
+    auto seen_box = [&](int jb) { return jb < s.n && (jb < s.sink_end || jb + box > s.lo); };
+    int pages = load_pages(k_begin), issued = 0;
+    bool ok_all = true;
+    for (int kb = k_begin; kb < k_end && ok_all; kb += per) {
+      const int next = load_pages(kb + per);
+      {
+        const int kk = kb + (lane >> nbl);
+        if (kk < k_end && seen_box(s.tile(kk) * PG_KEYS + (lane & (nbox - 1)) * box) &&
+            static_cast<uint32_t>(pages) >= static_cast<uint32_t>(p.num_pages)) {
+          record_status(HSTU_ERR_DEVICE_CHECK);
+          pages = -1;
         }
       }
-    };
-    auto load_side = [&](int kk, const int (&pg)[2], int64_t (&t)[2], float (&bd)[NB]) {
-      if (kk >= k_end) return;
-      const int j0 = s.tile(kk) * PG_KEYS;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int j = j0 + lane + 32 * e;
-        t[e] = t_last;  // past the last row: as the last event
-        if (s.seen(j)) {
-          if (static_cast<uint32_t>(pg[e]) < static_cast<uint32_t>(p.num_pages))
-            t[e] = p.ts[(static_cast<int64_t>(pg[e]) << psl) + (j & (ps - 1))];
-          else
-            record_status(HSTU_ERR_DEVICE_CHECK);
-          if (t_last - t[e] > PG_T0) record_status(HSTU_ERR_DEVICE_CHECK);
-        } else if (j < s.n) {
-          t[e] = t_last - PG_T0;  // a gap below the window: as old as can be
+      for (int kk = kb; kk < min(kb + per, k_end); ++kk) {
+        const int st = issued % PGS_STAGES;
+        int ok = 0;
+        if (lane == 0) {
+          ok = mbar_wait(&bar_empty[st], ((issued / PGS_STAGES) & 1) ^ 1, ctl) ? 1 : 0;
+          if (ok) mbar_arrive_expect_tx(&bar_full[st], 2 * PGS_TILE_BYTES);
         }
-      }
-      // entry x: i - j = (i0 + R - 1) - j0 - x, for column c and row r at x = c + R - 1 - r
+        if (!__shfl_sync(0xffffffffu, ok, 0)) {
+          ok_all = false;
+          break;
+        }
+        const int j0 = s.tile(kk) * PG_KEYS;
+        if ((lane >> nbl) == kk - kb) {
+          const int bx = lane & (nbox - 1);
+          const int64_t blk = static_cast<int64_t>(pages) * 2 * p.H + h;
+          const int32_t row = pages >= 0 ? static_cast<int32_t>((blk << psl) + ((j0 + bx * box) & (ps - 1))) : oob;
+          const int32_t row_v = pages >= 0 ? row + (p.H << psl) : oob;
+          uint8_t* dk = smem + PgsSmem::kK + st * PGS_TILE_BYTES + bx * box * 128;
+          tma_load_2d(dk, &tm_kv, &bar_full[st], 0, row);
+          tma_load_2d(dk + (PgsSmem::kV - PgsSmem::kK), &tm_kv, &bar_full[st], 0, row_v);
+        }
+        const uint32_t side = sbase + PgsSmem::kSide + st * PgsSmem::kSideBytes;
 #pragma unroll
-      for (int e = 0; e < NB; ++e) {
-        const int x = lane + 32 * e;
-        const int d = i0 + R - 1 - j0 - x;
-        if (x < kBand) bd[e] = kScale * __ldg(rp + min(max(d, 0), p.P - 1));
-      }
-    };
-    int pg0[2], pg1[2], pg2[2];
-    int64_t t0[2], t1[2];
-    float b0[NB], b1[NB];
-    load_pages(k_begin, pg0);
-    load_pages(k_begin + 1, pg1);
-    load_side(k_begin, pg0, t0, b0);
-    int issued = 0;
-    for (int kk = k_begin; kk < k_end; ++kk) {
-      const int st = issued % PGS_STAGES;
-      load_pages(kk + 2, pg2);
-      load_side(kk + 1, pg1, t1, b1);
-      int ok = 0;
-      if (lane == 0) ok = mbar_wait(&bar_empty[st], ((issued / PGS_STAGES) & 1) ^ 1, ctl) ? 1 : 0;
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      if (lane == 0) mbar_arrive_expect_tx(&bar_full[st], 2 * PGS_TILE_BYTES);
-      __syncwarp();
-      const int j0 = s.tile(kk) * PG_KEYS;
-      // a box's page: the one of its first seen position (parts that no row sees have none)
-      int page = -1;
-      for (int b = 0; b < nbox; ++b) {
-        const unsigned lo = __ballot_sync(0xffffffffu, (lane / box) == b && pg0[0] >= 0);
-        const unsigned hi = __ballot_sync(0xffffffffu, ((lane + 32) / box) == b && pg0[1] >= 0);
-        int v = -1;
-        if (lo) v = __shfl_sync(0xffffffffu, pg0[0], __ffs(lo) - 1);
-        else if (hi) v = __shfl_sync(0xffffffffu, pg0[1], __ffs(hi) - 1);
-        if (lane == b) page = v;
-      }
-      if (lane < nbox) {
-        const int jb = j0 + lane * box;
-        const bool pok = static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages);
-        const int32_t row = pok ? static_cast<int32_t>((((static_cast<int64_t>(page) * 2) * p.H + h) << psl) + (jb & (ps - 1))) : oob;
-        const int32_t row_v = pok ? row + (p.H << psl) : oob;
-        uint8_t* dk = smem + PgsSmem::kK + st * PGS_TILE_BYTES + lane * box * 128;
-        tma_load_2d(dk, &tm_kv, &bar_full[st], 0, row);
-        tma_load_2d(dk + (PgsSmem::kV - PgsSmem::kK), &tm_kv, &bar_full[st], 0, row_v);
-      }
-      ++issued;
-      int32_t* side_t = reinterpret_cast<int32_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
-      float* side_b = reinterpret_cast<float*>(side_t + 64);
+        for (int e = 0; e < 2; ++e) {
+          const int c = lane + 32 * e;
+          const int pg = __shfl_sync(0xffffffffu, pages, ((kk - kb) << nbl) + c / box);
+          const bool in = pg >= 0 && s.seen(j0 + c);
+          cp_async8(side + 8 * c, p.ts + (in ? (static_cast<int64_t>(pg) << psl) + ((j0 + c) & (ps - 1)) : 0),
+                    in ? 8u : 0u);
+        }
+        // entry x: i - j = (i0 + R - 1) - j0 - x, for column c and row r at x = c + R - 1 - r
 #pragma unroll
-      for (int e = 0; e < 2; ++e) side_t[lane + 32 * e] = paged_rel(t0[e], t_last);
-#pragma unroll
-      for (int e = 0; e < NB; ++e)
-        if (lane + 32 * e < kBand) side_b[lane + 32 * e] = b0[e];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_full[st]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        pg0[e] = pg1[e];
-        pg1[e] = pg2[e];
-        t0[e] = t1[e];
+        for (int x = lane; x < kBand; x += 32)
+          cp_async4(side + 64 * 8 + 4 * x, rp + min(max(i0 + R - 1 - j0 - x, 0), p.P - 1));
+        cp_async_arrive(&bar_full[st]);
+        ++issued;
       }
-#pragma unroll
-      for (int e = 0; e < NB; ++e) b0[e] = b1[e];
+      pages = next;
     }
     // every issued load lands before shared memory is reused or released
     if (lane == 0)
@@ -579,12 +564,13 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       if (!__all_sync(0xffffffffu, ok)) break;
       const int j0 = s.tile(kk) * PG_KEYS + wk;  // this warp's first key
       const uint32_t soff = st * PGS_TILE_BYTES;
-      const int32_t* side_t = reinterpret_cast<const int32_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
+      const int64_t* side_t = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
       const float* band = reinterpret_cast<const float*>(side_t + 64) + wk + R - 1;
       // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
       // times a NaN is a NaN, so they are cleared
-      const bool gap = j0 < s.lo && j0 + 16 > s.sink_end;
-      if (j0 + 16 > s.n || gap) {
+      // keys that no row sees among this warp's 16
+      const bool ragged = j0 + 16 > s.n || (j0 < s.lo && j0 + 16 > s.sink_end);
+      if (ragged) {
 #pragma unroll
         for (int e = lane; e < 16 * 8; e += 32)
           if (!s.seen(j0 + (e >> 3)))
@@ -611,15 +597,25 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         }
       }
       // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
-      int2 kt[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) kt[b] = *reinterpret_cast<const int2*>(side_t + wk + 8 * b + 2 * tq);
-      const int32_t kt_end = side_t[wk + 15];
-      bool steady = true;
+      // Time bucket of a row: it only falls along the keys, so while the chunk's last key
+      // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
+      // no row sees have no time: such chunks look every bucket up, and leave no bound.
+      const int32_t kt_end = paged_rel(side_t[wk + 15], t_last);
+      bool steady = !ragged;
 #pragma unroll
       for (int a = 0; a < 2 * MT; ++a) steady = steady && kt_end <= bound[a];
-      // times are not in order across a gap: buckets are looked up there and after it
-      steady = __all_sync(0xffffffffu, steady) && !gap;
+      steady = __all_sync(0xffffffffu, steady);
+      int2 kt[2];
+      if (!steady) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          kt[b].x = paged_rel(side_t[wk + 8 * b + 2 * tq], t_last);
+          kt[b].y = paged_rel(side_t[wk + 8 * b + 2 * tq + 1], t_last);
+        }
+        // the earliest visible event is among the CTA's first keys
+        if (it == 0 && lane < 16 && s.seen(j0 + lane) && t_last - side_t[wk + lane] > PG_T0)
+          record_status(HSTU_ERR_DEVICE_CHECK);
+      }
       // every row sees every key of this warp
       const int i_last = i0 + rows - 1;
       const bool full = j0 + 15 <= i0 &&
@@ -637,14 +633,14 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
             rt0 = time_bias_octave(ti[a] - kt[b].x, sOct, sOrt);
             rt1 = time_bias_octave(ti[a] - kt[b].y, sOct, sOrt);
           }
-          x[2 * b] = fmaf(sc[a >> 1][b][2 * (a & 1)], kScale, bp[0] + rt0);
-          x[2 * b + 1] = fmaf(sc[a >> 1][b][2 * (a & 1) + 1], kScale, bp[1] + rt1);
+          x[2 * b] = fmaf(sc[a >> 1][b][2 * (a & 1)] + bp[0], kScale, rt0);
+          x[2 * b + 1] = fmaf(sc[a >> 1][b][2 * (a & 1) + 1] + bp[1], kScale, rt1);
         }
         if (!steady) {
           // the bucket of the chunk's last key holds until a key passes its edge
           const int bk = time_bucket_octave(ti[a] - kt_end, sOct);
           rt[a] = sTime[bk];
-          bound[a] = gap ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
+          bound[a] = ragged ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
         }
         const int i = i0 + r;
         auto vis = [&](int e) {

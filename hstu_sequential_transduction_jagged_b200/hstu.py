@@ -155,12 +155,13 @@ def _check(status: int, where: str):
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 @dataclass
@@ -451,6 +452,9 @@ def stochastic_length(jag: Jagged, alpha: float, seed: int, step: int, x=None, s
     return out
 
 
+_CACHE_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+
+
 @dataclass
 class PagedCache:
     """A paged history cache: the caller's five device tensors (see hstu_cache_t)."""
@@ -473,15 +477,27 @@ class PagedCache:
             torch.zeros(num_pages, **i32), torch.full((num_seqs, max_blocks), -1, **i32),
             torch.zeros(num_seqs, **i32))
 
+    def __post_init__(self):
+        # the calls hand bare pointers on, so the layout is checked here
+        kv, ts, table = self.kv, self.timestamps, self.block_table
+        ks, bs = kv.shape, table.shape
+        if not (len(ks) == 6 and ks[2] == 2 and ks[5] == 64 and kv.dtype in _CACHE_DTYPE
+                and ts.shape == (ks[1], ks[4]) and ts.dtype == torch.int64
+                and self.ref_count.shape == (ks[1],) and len(bs) == 2
+                and self.lengths.shape == (bs[0],) and self.ref_count.dtype == torch.int32
+                and table.dtype == torch.int32 and self.lengths.dtype == torch.int32
+                and kv.is_contiguous() and ts.is_contiguous() and table.is_contiguous()
+                and self.ref_count.is_contiguous() and self.lengths.is_contiguous()):
+            raise ValueError("PagedCache: kv [L, pages, 2, H, page, 64] (fp16, bf16 or fp32), "
+                             "timestamps int64 [pages, page], ref_count int32 [pages], "
+                             "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous")
+
     def c(self) -> CacheT:
         L, pages, _, H, ps, _ = self.kv.shape
         return CacheT(L, H, _CACHE_DTYPE[self.kv.dtype], ps, pages, self.lengths.shape[0],
                       self.block_table.shape[1], self.kv.data_ptr(), self.timestamps.data_ptr(),
                       self.ref_count.data_ptr(), self.block_table.data_ptr(),
                       self.lengths.data_ptr())
-
-
-_CACHE_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
 def cache_workspace_bytes(cache: PagedCache, batch: int) -> int:
@@ -502,9 +518,11 @@ def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None
 
 
 def _rows_ld(t: torch.Tensor, what: str) -> int:
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1:
         raise ValueError(f"{what}: rows of contiguous elements are needed")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return st[0] if t.shape[0] > 1 else t.shape[1]
 
 
 def cache_append(cache: PagedCache, layer: int, chunk: Jagged, k, v, seq_ids=None, stream=None):
