@@ -228,19 +228,24 @@ AttnBwdFn attn_bwd_kernel_ptr(int phi, bool f16) {
 
 using PagedRowsFn = void (*)(const CUtensorMap, const PagedParams);
 
-template <bool F16, int MT>
+template <bool F16, int MH>
 PagedRowsFn paged_rows_kernel_for(int phi) {
   switch (phi) {
-    case HSTU_ACT_SILU: return hstu_paged_rows_kernel<HSTU_ACT_SILU, F16, MT>;
-    case HSTU_ACT_RELU: return hstu_paged_rows_kernel<HSTU_ACT_RELU, F16, MT>;
-    case HSTU_ACT_SOFTMAX: return hstu_paged_rows_kernel<HSTU_ACT_SOFTMAX, F16, MT>;
-    default: return hstu_paged_rows_kernel<HSTU_ACT_IDENTITY, F16, MT>;
+    case HSTU_ACT_SILU: return hstu_paged_rows_kernel<HSTU_ACT_SILU, F16, MH>;
+    case HSTU_ACT_RELU: return hstu_paged_rows_kernel<HSTU_ACT_RELU, F16, MH>;
+    case HSTU_ACT_SOFTMAX: return hstu_paged_rows_kernel<HSTU_ACT_SOFTMAX, F16, MH>;
+    default: return hstu_paged_rows_kernel<HSTU_ACT_IDENTITY, F16, MH>;
   }
 }
 
-PagedRowsFn paged_rows_kernel_ptr(int phi, bool f16, int mt) {
-  if (f16) return mt == 1 ? paged_rows_kernel_for<true, 1>(phi) : paged_rows_kernel_for<true, 2>(phi);
-  return mt == 1 ? paged_rows_kernel_for<false, 1>(phi) : paged_rows_kernel_for<false, 2>(phi);
+template <bool F16>
+PagedRowsFn paged_rows_kernel_halves(int phi, int mh) {
+  return mh == 1 ? paged_rows_kernel_for<F16, 1>(phi)
+                 : (mh == 2 ? paged_rows_kernel_for<F16, 2>(phi) : paged_rows_kernel_for<F16, 4>(phi));
+}
+
+PagedRowsFn paged_rows_kernel_ptr(int phi, bool f16, int mh) {
+  return f16 ? paged_rows_kernel_halves<true>(phi, mh) : paged_rows_kernel_halves<false>(phi, mh);
 }
 
 struct DeviceInfo {
@@ -278,8 +283,8 @@ hstu_status_t device_info(DeviceInfo** out) {
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, att_max));
     for (int phi = 0; phi < 4; ++phi)
       for (int f16 = 0; f16 < 2; ++f16)
-        for (int mt = 1; mt <= 2; ++mt)
-          HSTU_CHECK_CUDA(cudaFuncSetAttribute(paged_rows_kernel_ptr(phi, f16 != 0, mt),
+        for (int mh = 1; mh <= 4; mh *= 2)
+          HSTU_CHECK_CUDA(cudaFuncSetAttribute(paged_rows_kernel_ptr(phi, f16 != 0, mh),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(PgsSmem::kBytes)));
     const int g1 = static_cast<int>(F1Smem::kBytes);
@@ -1098,11 +1103,11 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
   if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, PG_KEYS), f16)) != HSTU_OK)
     return s;
-  const int mt = max_new <= 16 ? 1 : 2;
-  p.groups = (max_new + 16 * mt - 1) / (16 * mt);
+  const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
+  p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(ctas, 4 * di->sm_count, max_tiles, 2);
-  return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mt), ctas, p.nsplit, PGS_THREADS,
+  p.nsplit = paged_splits(ctas, 2 * di->sm_count, max_tiles, 2);
+  return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);
 }
 

@@ -22,6 +22,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "attn.cuh"
 
 namespace hstu {
@@ -273,7 +275,8 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 
 // ---------------------------------------------------------------- few rows
 
-// 16-bit operands, 16 * MT query rows per CTA, keys split over a cluster.  Bound
+// 16-bit operands, 8 * MH query rows per CTA (1, 2 or 4 halves of a 16-row MMA tile),
+// keys split over a cluster.  Bound
 // by the cache bandwidth, so the tensor work runs on warp-level MMAs (m16n8k16)
 // whose operands and results stay in registers: a 128-row tcgen05 tile would do
 // the element work of 128 rows for the 1..32 that exist.  Warp w of 4 owns keys
@@ -380,9 +383,10 @@ __device__ __forceinline__ void paged_store(const PagedParams& p, int64_t row, i
   }
 }
 
-template <int PHI, bool F16, int MT>
-__global__ void __launch_bounds__(PGS_THREADS)
+template <int PHI, bool F16, int MH>
+__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 3 : 2)
 hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ PagedParams p) {
+  constexpr int MT = (MH + 1) / 2;  // 16-row MMA tiles
   constexpr int R = 16 * MT;
   constexpr bool kSoftmax = PHI == HSTU_ACT_SOFTMAX;
   constexpr float kScale = phi_scale<PHI>();
@@ -519,7 +523,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
 
   // ---------------- compute warps
   float o[MT][8][4];
-  float m_run[2 * MT], l_run[2 * MT];
+  float m_run[MH], l_run[MH];
 #pragma unroll
   for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -527,15 +531,15 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[a][b][e] = 0.0f;
 #pragma unroll
-  for (int a = 0; a < 2 * MT; ++a) {
+  for (int a = 0; a < MH; ++a) {
     m_run[a] = -INFINITY;
     l_run[a] = 0.0f;
   }
   const int gr = lane >> 2, tq = lane & 3;  // row and column pair of the MMA fragments
   if (warp < PGS_WARPS) {
     uint32_t qf[MT][4][4];
-    int32_t ti[2 * MT], bound[2 * MT];
-    float rt[2 * MT];
+    int32_t ti[MH], bound[MH];
+    float rt[MH];
 #pragma unroll
     for (int a = 0; a < 2 * MT; ++a) {  // rows gr + 8 a
       const int r = gr + 8 * a;
@@ -547,9 +551,11 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         for (int e = 0; e < 2; ++e)
           qf[a >> 1][k][(a & 1) + 2 * e] =
               in ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * e + 2 * tq)) : 0u;
-      ti[a] = in ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
-      bound[a] = -1;  // the first chunk looks its buckets up
-      rt[a] = 0.0f;
+      if (a < MH) {
+        ti[a] = in ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
+        bound[a] = -1;  // the first chunk looks its buckets up
+        rt[a] = 0.0f;
+      }
     }
     const uint32_t sbase = smem_u32(smem);
     const int wk = warp * 16;  // this warp's keys of a tile
@@ -557,101 +563,140 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     const int krow = wk + ((lane >> 4) << 3) + (lane & 7), kch = (lane >> 3) & 1;
     const int vrow = wk + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
     const uint32_t kaddr = sbase + PgsSmem::kK + krow * 128, vaddr = sbase + PgsSmem::kV + vrow * 128;
+    const int i_last = i0 + rows - 1;
     int it = 0;
-    for (int kk = k_begin; kk < k_end; ++kk, ++it) {
-      const int st = it % PGS_STAGES;
-      const bool ok = mbar_wait(&bar_full[st], (it / PGS_STAGES) & 1, ctl);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int j0 = s.tile(kk) * PG_KEYS + wk;  // this warp's first key
-      const uint32_t soff = st * PGS_TILE_BYTES;
-      const int64_t* side_t = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
-      const float* band = reinterpret_cast<const float*>(side_t + 64) + wk + R - 1;
-      // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
-      // times a NaN is a NaN, so they are cleared
-      // keys that no row sees among this warp's 16
-      const bool ragged = j0 + 16 > s.n || (j0 < s.lo && j0 + 16 > s.sink_end);
-      if (ragged) {
+    // N tiles at a time, the k-th of the CTA being its it-th: independent chains of MMAs
+    // and element work that hide each other's latency.  False after a failed wait.
+    auto step = [&](auto n_c, int kk) -> bool {
+      constexpr int N = decltype(n_c)::value;
+      int j0[N];
+      uint32_t soff[N];
+      const int64_t* side_t[N];
+      float sc[N][MT][2][4];
+      uint32_t pf[N][MT][4];
+      bool ragged[N], steady[N], full[N], ok = true;
 #pragma unroll
-        for (int e = lane; e < 16 * 8; e += 32)
-          if (!s.seen(j0 + (e >> 3)))
-            *reinterpret_cast<uint4*>(smem + PgsSmem::kV + soff + (wk + (e >> 3)) * 128 + (e & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
+      for (int t = 0; t < N; ++t) {
+        const int st = (it + t) % PGS_STAGES;
+        ok = ok && mbar_wait(&bar_full[st], ((it + t) / PGS_STAGES) & 1, ctl);
+        j0[t] = s.tile(kk + t) * PG_KEYS + wk;  // this warp's first key
+        soff[t] = st * PGS_TILE_BYTES;
+        side_t[t] = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
+        // keys that no row sees among this warp's 16
+        ragged[t] = j0[t] + 16 > s.n || (j0[t] < s.lo && j0[t] + 16 > s.sink_end);
+        // every row sees every key of this warp
+        full[t] = j0[t] + 15 <= i0 && (p.window == 0 || j0[t] > i_last - p.window || j0[t] + 16 <= p.sinks);
       }
-      float sc[MT][2][4];
+      if (!__all_sync(0xffffffffu, ok)) return false;
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[a][b][e] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t kf[4];
-        ldsm_x4(kaddr + soff + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          mma_m16n8k16<F16>(sc[a][0], qf[a][k], kf[0], kf[1]);
-          mma_m16n8k16<F16>(sc[a][1], qf[a][k], kf[2], kf[3]);
+      for (int t = 0; t < N; ++t) {
+        // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
+        // times a NaN is a NaN, so they are cleared
+        if (ragged[t]) {
+          for (int e = lane; e < 16 * 8; e += 32)
+            if (!s.seen(j0[t] + (e >> 3)))
+              *reinterpret_cast<uint4*>(smem + PgsSmem::kV + soff[t] + (wk + (e >> 3)) * 128 + (e & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
       }
-      // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
-      // Time bucket of a row: it only falls along the keys, so while the chunk's last key
-      // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
-      // no row sees have no time: such chunks look every bucket up, and leave no bound.
-      const int32_t kt_end = paged_rel(side_t[wk + 15], t_last);
-      bool steady = !ragged;
 #pragma unroll
-      for (int a = 0; a < 2 * MT; ++a) steady = steady && kt_end <= bound[a];
-      steady = __all_sync(0xffffffffu, steady);
-      int2 kt[2];
-      if (!steady) {
+      for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          kt[b].x = paged_rel(side_t[wk + 8 * b + 2 * tq], t_last);
-          kt[b].y = paged_rel(side_t[wk + 8 * b + 2 * tq + 1], t_last);
-        }
-        // the earliest visible event is among the CTA's first keys
-        if (it == 0 && lane < 16 && s.seen(j0 + lane) && t_last - side_t[wk + lane] > PG_T0)
-          record_status(HSTU_ERR_DEVICE_CHECK);
-      }
-      // every row sees every key of this warp
-      const int i_last = i0 + rows - 1;
-      const bool full = j0 + 15 <= i0 &&
-                        (p.window == 0 || j0 > i_last - p.window || j0 + 16 <= p.sinks);
-      uint32_t pf[MT][4];
+        for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int a = 0; a < 2 * MT; ++a) {
-        const int r = gr + 8 * a;
-        float x[4];
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float* bp = band + 8 * b + 2 * tq - r;
-          float rt0 = rt[a], rt1 = rt[a];
-          if (!steady) {
-            rt0 = time_bias_octave(ti[a] - kt[b].x, sOct, sOrt);
-            rt1 = time_bias_octave(ti[a] - kt[b].y, sOct, sOrt);
+            for (int e = 0; e < 4; ++e) sc[t][a][b][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+          uint32_t kf[4];
+          ldsm_x4(kaddr + soff[t] + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
+#pragma unroll
+          for (int a = 0; a < MT; ++a) {
+            mma_m16n8k16<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
+            mma_m16n8k16<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
           }
-          x[2 * b] = fmaf(sc[a >> 1][b][2 * (a & 1)] + bp[0], kScale, rt0);
-          x[2 * b + 1] = fmaf(sc[a >> 1][b][2 * (a & 1) + 1] + bp[1], kScale, rt1);
         }
-        if (!steady) {
-          // the bucket of the chunk's last key holds until a key passes its edge
-          const int bk = time_bucket_octave(ti[a] - kt_end, sOct);
-          rt[a] = sTime[bk];
-          bound[a] = ragged ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
-        }
-        const int i = i0 + r;
-        auto vis = [&](int e) {
-          const int j = j0 + 8 * (e >> 1) + 2 * tq + (e & 1);
-          return j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
-        };
-        if constexpr (kSoftmax) {
-          if (!full)
+      // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = vis(e) ? x[e] : -INFINITY;
-          float cm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      for (int t = 0; t < N; ++t) {
+        const float* band = reinterpret_cast<const float*>(side_t[t] + 64) + wk + R - 1;
+        // Time bucket of a row: it only falls along the keys, so while the chunk's last key
+        // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
+        // no row sees have no time: such chunks look every bucket up, and leave no bound.
+        const int32_t kt_end = paged_rel(side_t[t][wk + 15], t_last);
+        steady[t] = !ragged[t];
+#pragma unroll
+        for (int a = 0; a < MH; ++a) steady[t] = steady[t] && kt_end <= bound[a];
+        steady[t] = __all_sync(0xffffffffu, steady[t]);
+        float rtv[MH][4];
+        if (steady[t]) {
+#pragma unroll
+          for (int a = 0; a < MH; ++a)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rtv[a][e] = rt[a];
+        } else {
+          // the earliest visible event is among the CTA's first keys
+          if (it == 0 && t == 0 && lane < 16 && s.seen(j0[t] + lane) && t_last - side_t[t][wk + lane] > PG_T0)
+            record_status(HSTU_ERR_DEVICE_CHECK);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int32_t kt = paged_rel(side_t[t][wk + 8 * (e >> 1) + 2 * tq + (e & 1)], t_last);
+#pragma unroll
+            for (int a = 0; a < MH; ++a) rtv[a][e] = time_bias_octave(ti[a] - kt, sOct, sOrt);
+          }
+#pragma unroll
+          for (int a = 0; a < MH; ++a) {
+            // the bucket of the chunk's last key holds until a key passes its edge
+            const int bk = time_bucket_octave(ti[a] - kt_end, sOct);
+            rt[a] = sTime[bk];
+            bound[a] = ragged[t] ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < MH; ++a) {
+          const int r = gr + 8 * a;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = fmaf(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] + band[8 * (e >> 1) + 2 * tq + (e & 1) - r],
+                        kScale, rtv[a][e]);
+          const int i = i0 + r;
+          auto vis = [&](int e) {
+            const int j = j0[t] + 8 * (e >> 1) + 2 * tq + (e & 1);
+            return j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
+          };
+          if constexpr (kSoftmax) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] = full[t] || vis(e) ? x[e] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (PHI == HSTU_ACT_SILU) x[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
+              else if constexpr (PHI == HSTU_ACT_RELU) x[e] = fmaxf(x[e], 0.0f);
+              if (!full[t]) x[e] = vis(e) ? x[e] : 0.0f;
+            }
+            // P in the operand type: the MMA takes both operands in one type
+            pf[t][a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
+            pf[t][a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
+          }
+        }
+      }
+      if constexpr (kSoftmax) {
+        // running maximum over the step's keys, then P = 2^(x - m); a warp's O is
+        // rescaled only when some row's maximum grew
+#pragma unroll
+        for (int a = 0; a < MH; ++a) {
+          float cm = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < N; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) cm = fmaxf(cm, sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)]);
           cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
           cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
           if (__any_sync(0xffffffffu, cm > m_run[a])) {
@@ -667,36 +712,46 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           }
           const float mm = m_run[a] > -INFINITY ? m_run[a] : 0.0f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = ex2_approx(x[e] - mm);
-            l_run[a] += x[e];
-          }
-        } else {
+          for (int t = 0; t < N; ++t) {
+            float x[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (PHI == HSTU_ACT_SILU) x[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
-            else if constexpr (PHI == HSTU_ACT_RELU) x[e] = fmaxf(x[e], 0.0f);
-            if (!full) x[e] = vis(e) ? x[e] : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+              x[e] = ex2_approx(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] - mm);
+              l_run[a] += x[e];
+            }
+            pf[t][a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
+            pf[t][a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
           }
         }
-        // P in the operand type: the MMA takes both operands in one type
-        pf[a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
-        pf[a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
       }
+      if constexpr (MH == 1)  // rows 8 .. 15 do not exist
+#pragma unroll
+        for (int t = 0; t < N; ++t) pf[t][0][1] = pf[t][0][3] = 0u;
       // ---- O += P V
 #pragma unroll
-      for (int b = 0; b < 8; b += 2) {
-        uint32_t vf[4];
-        ldsm_x4_t(vaddr + soff + (((b + vch) ^ (vrow & 7)) << 4), vf);
+      for (int t = 0; t < N; ++t)
 #pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          mma_m16n8k16<F16>(o[a][b], pf[a], vf[0], vf[1]);
-          mma_m16n8k16<F16>(o[a][b + 1], pf[a], vf[2], vf[3]);
+        for (int b = 0; b < 8; b += 2) {
+          uint32_t vf[4];
+          ldsm_x4_t(vaddr + soff[t] + (((b + vch) ^ (vrow & 7)) << 4), vf);
+#pragma unroll
+          for (int a = 0; a < MT; ++a) {
+            mma_m16n8k16<F16>(o[a][b], pf[t][a], vf[0], vf[1]);
+            mma_m16n8k16<F16>(o[a][b + 1], pf[t][a], vf[2], vf[3]);
+          }
         }
-      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_empty[st]);
-    }
+      if (lane == 0)
+#pragma unroll
+        for (int t = 0; t < N; ++t) mbar_arrive(&bar_empty[(it + t) % PGS_STAGES]);
+      it += N;
+      return true;
+    };
+    int kk = k_begin;
+    bool ok = true;
+    if constexpr (MT == 1)
+      for (; ok && kk + 1 < k_end; kk += 2) ok = step(std::integral_constant<int, 2>{}, kk);
+    for (; ok && kk < k_end; ++kk) ok = step(std::integral_constant<int, 1>{}, kk);
   }
   __syncthreads();  // the stages are idle: the partial sums go over them
   float* sO = reinterpret_cast<float*>(smem);
@@ -708,11 +763,11 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       for (int b = 0; b < 8; ++b)
         *reinterpret_cast<float2*>(sO + (warp * R + r) * PGS_OLD + 8 * b + 2 * tq) =
             make_float2(o[a >> 1][b][2 * (a & 1)], o[a >> 1][b][2 * (a & 1) + 1]);
-      if constexpr (kSoftmax) {
-        float l = l_run[a];
+      if (kSoftmax && a < MH) {
+        float l = l_run[a < MH ? a : 0];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (tq == 0) sMl[warp * 32 + r] = make_float2(m_run[a], l);
+        if (tq == 0) sMl[warp * 32 + r] = make_float2(m_run[a < MH ? a : 0], l);
       }
     }
   }
@@ -722,7 +777,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   const int c4 = tid & 15;
   const float inv_n = kSoftmax ? 1.0f : 1.0f / static_cast<float>(n_all);
   if (warp < PGS_WARPS) {
-    for (int r = tid >> 4; r < R; r += 8) {
+    for (int r = tid >> 4; r < 8 * MH; r += 8) {
       float f[PGS_WARPS], m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int w = 0; w < PGS_WARPS; ++w) f[w] = 1.0f;
@@ -759,7 +814,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   cluster.sync();
   if (warp < PGS_WARPS) {
     // rank `split` takes rows 8 split .., 8 (split + nsplit) ..
-    for (int r = 8 * split + (tid >> 4); r < R; r += 8 * p.nsplit) {
+    for (int r = 8 * split + (tid >> 4); r < 8 * MH; r += 8 * p.nsplit) {
       float m = -INFINITY, l = 0.0f;
       if constexpr (kSoftmax)
         for (int k = 0; k < p.nsplit; ++k) m = fmaxf(m, cluster.map_shared_rank(sMlC, k)[r].x);
