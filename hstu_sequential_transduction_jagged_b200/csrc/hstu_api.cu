@@ -899,7 +899,7 @@ hstu_status_t check_cache(const hstu_cache_t* c, bool refs) {
   if (c->kv == nullptr || c->timestamps == nullptr || c->block_table == nullptr ||
       c->lengths == nullptr || (refs && c->ref_count == nullptr))
     return HSTU_ERR_INVALID_ARGUMENT;
-  if (!aligned16(c->kv)) return HSTU_ERR_INVALID_ARGUMENT;
+  if (!aligned16(c->kv) || !aligned16(c->timestamps)) return HSTU_ERR_INVALID_ARGUMENT;
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return HSTU_ERR_UNSUPPORTED;
   // one layer's page rows are a tensor-map coordinate; positions are int32
@@ -1032,7 +1032,7 @@ hstu_status_t launch_cluster(Fn fn, int64_t ctas, int ns, int threads, size_t sm
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   lc.attrs = at;
-  lc.numAttrs = 1;
+  lc.numAttrs = ns > 1 ? 1 : 0;
   HSTU_CHECK_CUDA(cudaLaunchKernelEx(&lc, fn, args...));
   return HSTU_OK;
 }
@@ -1090,23 +1090,23 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   // the longest visible part of a context, in key tiles
   int64_t seen = p.max_context;
   if (p.window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(p.window) + max_new + p.sinks);
-  const int max_tiles = static_cast<int>((seen + PG_KEYS - 1) / PG_KEYS);
+  auto tiles_of = [&](int keys) { return static_cast<int>((seen + keys - 1) / keys); };
   ProfScope prof(K_PAGED_ATTN, st);
   if (ca->dtype == HSTU_FP32) {
     p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(ctas, 2 * di->sm_count, max_tiles, 1);
+    p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PG32_KEYS), 1);
     return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
   }
   const bool f16 = ca->dtype == HSTU_FP16;
   CUtensorMap mkv;
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
-  if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, PG_KEYS), f16)) != HSTU_OK)
+  if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, 64), f16)) != HSTU_OK)
     return s;
   const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
   p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(ctas, 2 * di->sm_count, max_tiles, 2);
+  p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PGS_KEYS), 1);
   return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);
 }

@@ -53,11 +53,12 @@ struct PagedParams {
   int4 oct[32];
 };
 
-constexpr int PG_KEYS = 64;  // keys per tile
 
 __device__ __forceinline__ int log2_small(int v) { return 31 - __clz(v); }
 
-// One sequence's part of a launch, the same for every CTA of its clusters.
+// One sequence's part of a launch, the same for every CTA of its clusters; tiles of
+// KEYS keys.
+template <int KEYS>
 struct PagedSeq {
   int seq, n, c;       // table row, events, new events
   int64_t q0;          // first query row
@@ -75,7 +76,8 @@ struct PagedSeq {
 
 // Reads and checks sequence u; r0 / r1: the query rows [r0, r1) of this row group.
 // Returns 1 to go on, 0 when the group has no rows, -1 when the input is bad.
-__device__ __forceinline__ int paged_seq(const PagedParams& p, int u, int r0, int rows, PagedSeq& s) {
+template <int KEYS>
+__device__ __forceinline__ int paged_seq(const PagedParams& p, int u, int r0, int rows, PagedSeq<KEYS>& s) {
   const int64_t o0 = p.q_offsets[u], o1 = p.q_offsets[u + 1];
   const int64_t cnt = o1 - o0;
   if (cnt == 0) return 0;
@@ -90,9 +92,9 @@ __device__ __forceinline__ int paged_seq(const PagedParams& p, int u, int r0, in
   const int i1 = s.n - s.c + min(r0 + rows, s.c);  // one past the last row's
   s.lo = p.window > 0 ? max(0, i0 - p.window + 1) : 0;
   s.sink_end = min(p.sinks, s.lo);
-  s.first = s.lo / PG_KEYS;
-  s.n_sink = min((s.sink_end + PG_KEYS - 1) / PG_KEYS, s.first);
-  s.n_tiles = s.n_sink + (i1 + PG_KEYS - 1) / PG_KEYS - s.first;
+  s.first = s.lo / KEYS;
+  s.n_sink = min((s.sink_end + KEYS - 1) / KEYS, s.first);
+  s.n_tiles = s.n_sink + (i1 + KEYS - 1) / KEYS - s.first;
   s.n = i1;  // keys past the group's last row are seen by none of its rows
   return 1;
 }
@@ -110,18 +112,19 @@ __device__ __forceinline__ int32_t paged_rel(int64_t t, int64_t t_last) {
 // 64-key tiles in shared memory, 16 query rows per CTA, thread (key or column
 // tid % 64, rows tid / 64 + 4 k).  Exact exponentials (expf), so the result holds
 // fp32 accuracy.  Softmax keeps a running maximum and sum per row.
+constexpr int PG32_KEYS = 64;
 constexpr int PG32_ROWS = 16;
 constexpr int PG32_THREADS = 256;
 
 struct Paged32Smem {
   float q[PG32_ROWS][64];
-  float k[PG_KEYS][65];
-  float v[PG_KEYS][64];
-  float s[PG32_ROWS][PG_KEYS + 1];
+  float k[PG32_KEYS][65];
+  float v[PG32_KEYS][64];
+  float s[PG32_ROWS][PG32_KEYS + 1];
   float o[PG32_ROWS][64];       // this CTA's partial sums
   float2 ml[PG32_ROWS];         // softmax: (max, sum) of this CTA's keys
   float scale[PG32_ROWS];       // softmax: factor of the running sums
-  int32_t kt[PG_KEYS];
+  int32_t kt[PG32_KEYS];
   int32_t qt[PG32_ROWS];
   float rt[MAX_TIME_BUCKETS];
 };
@@ -135,7 +138,7 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
   const int h = static_cast<int>(id % p.H);
   const int g = static_cast<int>((id / p.H) % p.groups), u = static_cast<int>(id / p.H / p.groups);
   const int tid = threadIdx.x;
-  PagedSeq s;
+  PagedSeq<PG32_KEYS> s;
   const int r0 = g * PG32_ROWS;
   const int go = paged_seq(p, u, r0, PG32_ROWS, s);
   if (go <= 0) {  // the same for the whole cluster
@@ -164,10 +167,10 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
   const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
   const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
   for (int kk = k_begin; kk < k_end; ++kk) {
-    const int j0 = s.tile(kk) * PG_KEYS;
+    const int j0 = s.tile(kk) * PG32_KEYS;
     __syncthreads();
     // the tile's rows, 16 bytes per thread and step; keys that no row sees are zeros
-    for (int e = tid; e < 2 * PG_KEYS * 16; e += PG32_THREADS) {
+    for (int e = tid; e < 2 * PG32_KEYS * 16; e += PG32_THREADS) {
       const int kv = e >> 10, r = (e >> 4) & 63, c4 = e & 15;
       const int j = j0 + r;
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -188,7 +191,7 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
         *reinterpret_cast<float4*>(&sm.v[r][4 * c4]) = x;
       }
     }
-    if (tid < PG_KEYS) {
+    if (tid < PG32_KEYS) {
       const int j = j0 + tid;
       int32_t t = 0;
       if (s.seen(j)) {
@@ -222,10 +225,10 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
     if (softmax) {
       if (tid < PG32_ROWS) {
         float m = sm.ml[tid].x;
-        for (int c = 0; c < PG_KEYS; ++c) m = fmaxf(m, sm.s[tid][c]);
+        for (int c = 0; c < PG32_KEYS; ++c) m = fmaxf(m, sm.s[tid][c]);
         const float f = m > -INFINITY ? expf(sm.ml[tid].x - m) : 1.0f;
         float l = sm.ml[tid].y * f;
-        for (int c = 0; c < PG_KEYS; ++c) {
+        for (int c = 0; c < PG32_KEYS; ++c) {
           const float e = m > -INFINITY ? expf(sm.s[tid][c] - m) : 0.0f;
           sm.s[tid][c] = e;
           l += e;
@@ -239,7 +242,7 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
     }
     // each tile's sum apart, then added: the rounding grows with the tiles, not the keys
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < PG_KEYS; ++c) {
+    for (int c = 0; c < PG32_KEYS; ++c) {
       const float vv = sm.v[c][col];
 #pragma unroll
       for (int a = 0; a < 4; ++a) part[a] = fmaf(sm.s[rg + 4 * a][c], vv, part[a]);
@@ -279,28 +282,29 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 // keys split over a cluster.  Bound
 // by the cache bandwidth, so the tensor work runs on warp-level MMAs (m16n8k16)
 // whose operands and results stay in registers: a 128-row tcgen05 tile would do
-// the element work of 128 rows for the 1..32 that exist.  Warp w of 4 owns keys
-// 16 w .. 16 w + 15 of every 64-key tile for all the rows: S = Q K^T, the element
-// work and O += P V need no exchange between warps until the end.  A fifth warp
+// the element work of 128 rows for the 1..32 that exist.  Warp w of 8 owns keys
+// 16 w .. 16 w + 15 of every 128-key tile for all the rows: S = Q K^T, the element
+// work and O += P V need no exchange between warps until the end.  A ninth warp
 // streams K, V (TMA, one box per page part, 128B swizzle), key times and the
 // position band (cp.async) through a ring of stages, and never waits for a value it
 // loads: block-table entries come 32 boxes at a time, a batch ahead.
-constexpr int PGS_WARPS = 4;
+constexpr int PGS_KEYS = 128;  // keys per tile, 16 per warp
+constexpr int PGS_WARPS = 8;
 constexpr int PGS_THREADS = (PGS_WARPS + 1) * 32;
-constexpr int PGS_STAGES = 4;
-constexpr uint32_t PGS_TILE_BYTES = PG_KEYS * 128;
+constexpr int PGS_STAGES = 3;
+constexpr uint32_t PGS_TILE_BYTES = PGS_KEYS * 128;
 constexpr int PGS_OLD = 68;  // row stride (floats) of the partial sums: 16-byte rows, no bank conflicts
 
 struct PgsSmem {
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kV = kK + PGS_STAGES * PGS_TILE_BYTES;
-  static constexpr uint32_t kSide = kV + PGS_STAGES * PGS_TILE_BYTES;  // per stage: 64 times, 96 biases
-  static constexpr uint32_t kSideBytes = 64 * 8 + 96 * 4;
+  static constexpr uint32_t kSide = kV + PGS_STAGES * PGS_TILE_BYTES;  // per stage: times, biases
+  static constexpr uint32_t kSideBytes = PGS_KEYS * 8 + (PGS_KEYS + 32 + 8) * 4;
   static constexpr uint32_t kTime = kSide + PGS_STAGES * kSideBytes;
   static constexpr uint32_t kThr = kTime + MAX_TIME_BUCKETS * 4;
   static constexpr uint32_t kOct = kThr + MAX_TIME_BUCKETS * 4;
   static constexpr uint32_t kOrt = kOct + 32 * 16;
-  static constexpr uint32_t kMl = kOrt + 32 * 16;                  // 4 warps x 32 rows float2
+  static constexpr uint32_t kMl = kOrt + 32 * 16;                  // warps x 32 rows float2
   static constexpr uint32_t kMlC = kMl + PGS_WARPS * 32 * 8;       // 32 rows float2 of the CTA
   static constexpr uint32_t kBars = kMlC + 32 * 8;
   static constexpr uint32_t kAbort = kBars + 2 * PGS_STAGES * 8;
@@ -308,18 +312,34 @@ struct PgsSmem {
   static_assert(PGS_WARPS * 32 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
 };
 
-// Asynchronous copies of 8 and 4 bytes; with `bytes` 0 the destination is zeroed.
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Copy of `bytes` contiguous bytes (16-byte aligned, a multiple of 16) completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// tma_load_2d to a shared-memory address.
+__device__ __forceinline__ void tma_load_2d_to(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
+                                               int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
 }
 // One arrival on the barrier (counted in its expected arrivals) when this
 // thread's asynchronous copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+
+// First offset i - j of a tile's position band: the last key's for the first row, down
+// to a multiple of 4 (16 bytes); d = i0 - j0.
+__device__ __forceinline__ int paged_band0(int d, int keys) { return (d - (keys - 1)) & ~3; }
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -349,6 +369,24 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// D = A B: the first step of a chain.
+template <bool F16>
+__device__ __forceinline__ void mma_m16n8k16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                   uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 template <bool F16>
@@ -384,13 +422,13 @@ __device__ __forceinline__ void paged_store(const PagedParams& p, int64_t row, i
 }
 
 template <int PHI, bool F16, int MH>
-__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 2 : 1)
 hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ PagedParams p) {
   constexpr int MT = (MH + 1) / 2;  // 16-row MMA tiles
   constexpr int R = 16 * MT;
   constexpr bool kSoftmax = PHI == HSTU_ACT_SOFTMAX;
   constexpr float kScale = phi_scale<PHI>();
-  constexpr int kBand = PG_KEYS + R;  // biases of a tile (one unused)
+  constexpr int kBand = PGS_KEYS + R + 4;  // biases of a tile, from a multiple of 4 down
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   namespace cg = cooperative_groups;
   // the same offset in every CTA of a cluster: shared memory is read across it
@@ -400,7 +438,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   const int h = static_cast<int>(id % p.H);
   const int g = static_cast<int>((id / p.H) % p.groups), u = static_cast<int>(id / p.H / p.groups);
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
-  PagedSeq s;
+  PagedSeq<PGS_KEYS> s;
   const int r0 = g * R;
   const int go = paged_seq(p, u, r0, R, s);
   if (go <= 0) {  // the same for the whole cluster, before any barrier
@@ -428,17 +466,6 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     *sAbort = 0;
     fence_mbar_init();
   }
-  const float* rt_g = p.rab_time + static_cast<int64_t>(h) * p.Tb;
-  for (int k = tid; k < p.Tb; k += PGS_THREADS) {
-    sTime[k] = kScale * rt_g[k];
-    sThr[k] = p.thr[k];
-  }
-  if (tid < 32) {
-    const int4 o = p.oct[tid];
-    auto tb = [&](int b) { return kScale * rt_g[min(max(b, 0), p.Tb - 1)]; };
-    sOct[tid] = o;
-    sOrt[tid] = make_float4(tb(o.w), tb(o.w + 1), tb(o.w + 2), tb(o.w + 3));
-  }
   __syncthreads();
   const WaitCtl ctl{sAbort, p.timeout_ns};
   const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
@@ -449,70 +476,94 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
     const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
     const int psl = p.ps_log2, ps = 1 << psl;
-    const int box = min(ps, PG_KEYS), nbox = PG_KEYS / box;
+    const int boxl = min(psl, 6), box = 1 << boxl;  // rows of a box: a page or 64 rows of one
+    const int nbl = 7 - boxl;                       // log2 of the boxes of a tile
     const int32_t oob = static_cast<int32_t>((static_cast<int64_t>(p.num_pages) * 2 * p.H) << psl);
-    const int nbl = log2_small(nbox), per = 32 >> nbl;  // tiles per batch of block-table entries
-    const uint32_t sbase = smem_u32(smem);
-    // the page of box (lane % nbox) of tile k0 + lane / nbox; -1 where no row sees
-    // it (its rows are read as zeros), and where a page is missing, which is reported
-    auto load_pages = [&](int k0) -> int {
-      const int kk = k0 + (lane >> nbl);
-      if (kk >= k_end) return -1;
-      const int jb = s.tile(kk) * PG_KEYS + (lane & (nbox - 1)) * box;
-      if (jb >= s.n || (jb >= s.sink_end && jb + box <= s.lo)) return -1;
-      return tab[jb >> psl];
+    const int per = 32 >> nbl;  // tiles per batch of block-table entries
+    const int bx = lane & ((1 << nbl) - 1);
+    // One lane's box of a batch: the page of box bx of tile k0 + lane / boxes
+    struct Box {
+      int page;  // -1: no row sees it
+      int j;     // its first position
     };
-    auto seen_box = [&](int jb) { return jb < s.n && (jb < s.sink_end || jb + box > s.lo); };
-    int pages = load_pages(k_begin), issued = 0;
+    auto load_box = [&](int k0) -> Box {
+      Box b{-1, 0};
+      const int kk = k0 + (lane >> nbl);
+      if (kk >= k_end) return b;
+      b.j = s.tile(kk) * PGS_KEYS + (bx << boxl);
+      if (b.j < s.n && (b.j < s.sink_end || b.j + box > s.lo)) {
+        b.page = tab[b.j >> psl];
+        if (b.page < 0) b.page = INT32_MAX;  // seen, and no page
+      }
+      return b;
+    };
+    Box cur = load_box(k_begin);
+    int st = 0, issued = 0;
+    uint32_t ph = 1;
     bool ok_all = true;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t box_dst = sbase + PgsSmem::kK + (bx << boxl) * 128;
+    const uint32_t side0 = sbase + PgsSmem::kSide;
+    const bool rp16 = (reinterpret_cast<uintptr_t>(rp) & 15u) == 0;
     for (int kb = k_begin; kb < k_end && ok_all; kb += per) {
-      const int next = load_pages(kb + per);
-      {
-        const int kk = kb + (lane >> nbl);
-        if (kk < k_end && seen_box(s.tile(kk) * PG_KEYS + (lane & (nbox - 1)) * box) &&
-            static_cast<uint32_t>(pages) >= static_cast<uint32_t>(p.num_pages)) {
+      const Box next = load_box(kb + per);
+      // tensor-map rows of the lane's box (rows past the tensor read as zeros) and
+      // the index of its first timestamp, -1 where there is none
+      int32_t row_k = oob, row_v = oob, ts0 = -1;
+      if (cur.page >= 0) {
+        if (cur.page < p.num_pages) {
+          const int32_t slot = cur.j & (ps - 1);
+          row_k = ((cur.page * 2 * p.H + h) << psl) + slot;
+          row_v = row_k + (p.H << psl);
+          ts0 = (cur.page << psl) + slot;
+        } else {
           record_status(HSTU_ERR_DEVICE_CHECK);
-          pages = -1;
         }
       }
-      for (int kk = kb; kk < min(kb + per, k_end); ++kk) {
-        const int st = issued % PGS_STAGES;
+      const unsigned with_ts = __ballot_sync(0xffffffffu, ts0 >= 0);
+      const int n_here = min(per, k_end - kb);
+      for (int t = 0; t < n_here; ++t) {
+        // Biases by position, ascending from entry 0 at offset d4: row r and column c
+        // are at y = (i0 + r) - (j0 + c) - d4.  One copy inside the table, lane by
+        // lane where the offsets leave it and clamp.
+        const int j0 = s.tile(kb + t) * PGS_KEYS;
+        const int d4 = paged_band0(i0 - j0, PGS_KEYS);
+        const bool bulk = rp16 && d4 >= 0 && d4 + kBand <= p.P;
         int ok = 0;
         if (lane == 0) {
-          ok = mbar_wait(&bar_empty[st], ((issued / PGS_STAGES) & 1) ^ 1, ctl) ? 1 : 0;
-          if (ok) mbar_arrive_expect_tx(&bar_full[st], 2 * PGS_TILE_BYTES);
+          ok = mbar_wait(&bar_empty[st], ph, ctl) ? 1 : 0;
+          if (ok) {
+            const unsigned mine = (with_ts >> (t << nbl)) & ((1u << (1 << nbl)) - 1u);
+            mbar_arrive_expect_tx(&bar_full[st], 2 * PGS_TILE_BYTES + (__popc(mine) << (boxl + 3)) +
+                                                     (bulk ? kBand * 4 : 0));
+          }
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) {
           ok_all = false;
           break;
         }
-        const int j0 = s.tile(kk) * PG_KEYS;
-        if ((lane >> nbl) == kk - kb) {
-          const int bx = lane & (nbox - 1);
-          const int64_t blk = static_cast<int64_t>(pages) * 2 * p.H + h;
-          const int32_t row = pages >= 0 ? static_cast<int32_t>((blk << psl) + ((j0 + bx * box) & (ps - 1))) : oob;
-          const int32_t row_v = pages >= 0 ? row + (p.H << psl) : oob;
-          uint8_t* dk = smem + PgsSmem::kK + st * PGS_TILE_BYTES + bx * box * 128;
-          tma_load_2d(dk, &tm_kv, &bar_full[st], 0, row);
-          tma_load_2d(dk + (PgsSmem::kV - PgsSmem::kK), &tm_kv, &bar_full[st], 0, row_v);
+        const uint32_t side = side0 + st * PgsSmem::kSideBytes;
+        if ((lane >> nbl) == t) {
+          const uint32_t dst = box_dst + st * PGS_TILE_BYTES;
+          tma_load_2d_to(dst, &tm_kv, &bar_full[st], 0, row_k);
+          tma_load_2d_to(dst + (PgsSmem::kV - PgsSmem::kK), &tm_kv, &bar_full[st], 0, row_v);
+          // a part's times, unwritten slots and all: only those of seen keys are used
+          if (ts0 >= 0) bulk_load(side + (bx << (boxl + 3)), p.ts + ts0, 8u << boxl, &bar_full[st]);
         }
-        const uint32_t side = sbase + PgsSmem::kSide + st * PgsSmem::kSideBytes;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int c = lane + 32 * e;
-          const int pg = __shfl_sync(0xffffffffu, pages, ((kk - kb) << nbl) + c / box);
-          const bool in = pg >= 0 && s.seen(j0 + c);
-          cp_async8(side + 8 * c, p.ts + (in ? (static_cast<int64_t>(pg) << psl) + ((j0 + c) & (ps - 1)) : 0),
-                    in ? 8u : 0u);
+        const uint32_t band = side + PGS_KEYS * 8;
+        if (bulk) {
+          if (lane == 0) bulk_load(band, rp + d4, kBand * 4, &bar_full[st]);
+        } else {
+          for (int y = lane; y < kBand; y += 32) cp_async4(band + 4 * y, rp + min(max(d4 + y, 0), p.P - 1));
         }
-        // entry x: i - j = (i0 + R - 1) - j0 - x, for column c and row r at x = c + R - 1 - r
-#pragma unroll
-        for (int x = lane; x < kBand; x += 32)
-          cp_async4(side + 64 * 8 + 4 * x, rp + min(max(i0 + R - 1 - j0 - x, 0), p.P - 1));
         cp_async_arrive(&bar_full[st]);
         ++issued;
+        if (++st == PGS_STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
-      pages = next;
+      cur = next;
     }
     // every issued load lands before shared memory is reused or released
     if (lane == 0)
@@ -537,8 +588,22 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   }
   const int gr = lane >> 2, tq = lane & 3;  // row and column pair of the MMA fragments
   if (warp < PGS_WARPS) {
+    // bias tables, while the first tiles are on their way
+    const float* rt_g = p.rab_time + static_cast<int64_t>(h) * p.Tb;
+    for (int k = tid; k < p.Tb; k += PGS_WARPS * 32) {
+      sTime[k] = kScale * __ldg(rt_g + k);
+      sThr[k] = p.thr[k];
+    }
+    if (tid < 32) {
+      const int4 o4 = p.oct[tid];
+      auto tb = [&](int b) { return kScale * __ldg(rt_g + min(max(b, 0), p.Tb - 1)); };
+      sOct[tid] = o4;
+      sOrt[tid] = make_float4(tb(o4.w), tb(o4.w + 1), tb(o4.w + 2), tb(o4.w + 3));
+    }
+    named_barrier_sync(1, PGS_WARPS * 32);
     uint32_t qf[MT][4][4];
-    int32_t ti[MH], bound[MH];
+    int32_t ti[MH];
+    int64_t bound[MH];  // latest time still in the row's current bucket
     float rt[MH];
 #pragma unroll
     for (int a = 0; a < 2 * MT; ++a) {  // rows gr + 8 a
@@ -553,7 +618,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
               in ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * e + 2 * tq)) : 0u;
       if (a < MH) {
         ti[a] = in ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
-        bound[a] = -1;  // the first chunk looks its buckets up
+        bound[a] = INT64_MIN;  // the first chunk looks its buckets up
         rt[a] = 0.0f;
       }
     }
@@ -564,9 +629,11 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     const int vrow = wk + (((lane >> 3) & 1) << 3) + (lane & 7), vch = lane >> 4;
     const uint32_t kaddr = sbase + PgsSmem::kK + krow * 128, vaddr = sbase + PgsSmem::kV + vrow * 128;
     const int i_last = i0 + rows - 1;
+    // the tiles [f_lo, f_hi) of the list that every row sees whole
+    const int f_lo = p.window == 0 ? 0 : s.n_sink + max(0, (i_last - p.window + PGS_KEYS) / PGS_KEYS - s.first);
+    const int f_hi = s.n_sink + (i0 + 1) / PGS_KEYS - s.first;
     int it = 0;
-    // N tiles at a time, the k-th of the CTA being its it-th: independent chains of MMAs
-    // and element work that hide each other's latency.  False after a failed wait.
+    // N tiles, the k-th of the list on being the CTA's it-th on; false after a failed wait
     auto step = [&](auto n_c, int kk) -> bool {
       constexpr int N = decltype(n_c)::value;
       int j0[N];
@@ -579,13 +646,16 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       for (int t = 0; t < N; ++t) {
         const int st = (it + t) % PGS_STAGES;
         ok = ok && mbar_wait(&bar_full[st], ((it + t) / PGS_STAGES) & 1, ctl);
-        j0[t] = s.tile(kk + t) * PG_KEYS + wk;  // this warp's first key
+        j0[t] = s.tile(kk + t) * PGS_KEYS + wk;  // this warp's first key
         soff[t] = st * PGS_TILE_BYTES;
         side_t[t] = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
-        // keys that no row sees among this warp's 16
-        ragged[t] = j0[t] + 16 > s.n || (j0[t] < s.lo && j0[t] + 16 > s.sink_end);
-        // every row sees every key of this warp
-        full[t] = j0[t] + 15 <= i0 && (p.window == 0 || j0[t] > i_last - p.window || j0[t] + 16 <= p.sinks);
+        // every row sees every key of this warp; some key is seen by no row
+        full[t] = true;
+        ragged[t] = false;
+        if (kk + t < f_lo || kk + t >= f_hi) {
+          full[t] = j0[t] + 15 <= i0 && (p.window == 0 || j0[t] > i_last - p.window || j0[t] + 16 <= p.sinks);
+          ragged[t] = j0[t] + 16 > s.n || (j0[t] < s.lo && j0[t] + 16 > s.sink_end);
+        }
       }
       if (!__all_sync(0xffffffffu, ok)) return false;
 #pragma unroll
@@ -602,14 +672,6 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         }
       }
 #pragma unroll
-      for (int t = 0; t < N; ++t)
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[t][a][b][e] = 0.0f;
-#pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int t = 0; t < N; ++t) {
@@ -617,21 +679,29 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           ldsm_x4(kaddr + soff[t] + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
 #pragma unroll
           for (int a = 0; a < MT; ++a) {
-            mma_m16n8k16<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
-            mma_m16n8k16<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
+            if (k == 0) {
+              mma_m16n8k16_first<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
+              mma_m16n8k16_first<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
+            } else {
+              mma_m16n8k16<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
+              mma_m16n8k16<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
+            }
           }
         }
       // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        const float* band = reinterpret_cast<const float*>(side_t[t] + 64) + wk + R - 1;
+        // row 0, column 0 of this warp
+        const int j_tile = j0[t] - wk;
+        const float* band = reinterpret_cast<const float*>(side_t[t] + PGS_KEYS) + (i0 - j0[t]) -
+                            paged_band0(i0 - j_tile, PGS_KEYS);
         // Time bucket of a row: it only falls along the keys, so while the chunk's last key
         // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
         // no row sees have no time: such chunks look every bucket up, and leave no bound.
-        const int32_t kt_end = paged_rel(side_t[t][wk + 15], t_last);
+        const int64_t t_end = side_t[t][wk + 15];
         steady[t] = !ragged[t];
 #pragma unroll
-        for (int a = 0; a < MH; ++a) steady[t] = steady[t] && kt_end <= bound[a];
+        for (int a = 0; a < MH; ++a) steady[t] = steady[t] && t_end <= bound[a];
         steady[t] = __all_sync(0xffffffffu, steady[t]);
         float rtv[MH][4];
         if (steady[t]) {
@@ -652,9 +722,9 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
 #pragma unroll
           for (int a = 0; a < MH; ++a) {
             // the bucket of the chunk's last key holds until a key passes its edge
-            const int bk = time_bucket_octave(ti[a] - kt_end, sOct);
+            const int bk = time_bucket_octave(ti[a] - paged_rel(t_end, t_last), sOct);
             rt[a] = sTime[bk];
-            bound[a] = ragged[t] ? -1 : (bk == 0 ? INT32_MAX : ti[a] - sThr[bk]);
+            bound[a] = ragged[t] ? INT64_MIN : (bk == 0 ? INT64_MAX : t_last - PG_T0 + (ti[a] - sThr[bk]));
           }
         }
 #pragma unroll
@@ -663,7 +733,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[e] = fmaf(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] + band[8 * (e >> 1) + 2 * tq + (e & 1) - r],
+            x[e] = fmaf(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] + band[r - (8 * (e >> 1) + 2 * tq + (e & 1))],
                         kScale, rtv[a][e]);
           const int i = i0 + r;
           auto vis = [&](int e) {
@@ -749,8 +819,6 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     };
     int kk = k_begin;
     bool ok = true;
-    if constexpr (MT == 1)
-      for (; ok && kk + 1 < k_end; kk += 2) ok = step(std::integral_constant<int, 2>{}, kk);
     for (; ok && kk < k_end; ++kk) ok = step(std::integral_constant<int, 1>{}, kk);
   }
   __syncthreads();  // the stages are idle: the partial sums go over them
@@ -772,12 +840,12 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     }
   }
   __syncthreads();
-  // the CTA's sums over its four warps, in place of warp 0's (8 rows x 16 lanes a step)
+  // the CTA's sums over its warps, in place of warp 0's (16 rows x 16 lanes a step)
   const bool alone = p.nsplit == 1;
   const int c4 = tid & 15;
   const float inv_n = kSoftmax ? 1.0f : 1.0f / static_cast<float>(n_all);
   if (warp < PGS_WARPS) {
-    for (int r = tid >> 4; r < 8 * MH; r += 8) {
+    for (int r = tid >> 4; r < 8 * MH; r += 16) {
       float f[PGS_WARPS], m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int w = 0; w < PGS_WARPS; ++w) f[w] = 1.0f;
@@ -813,8 +881,11 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   if (warp < PGS_WARPS) {
-    // rank `split` takes rows 8 split .., 8 (split + nsplit) ..
-    for (int r = 8 * split + (tid >> 4); r < 8 * MH; r += 8 * p.nsplit) {
+    // rank `split` takes rows split, split + nsplit, .. (16 lanes a row; every lane of a
+    // warp goes through the same steps)
+    for (int base = 0; base < 8 * MH; base += 16 * p.nsplit) {
+      const int r_of = base + split + p.nsplit * (tid >> 4);
+      const int r = min(r_of, 8 * MH - 1);
       float m = -INFINITY, l = 0.0f;
       if constexpr (kSoftmax)
         for (int k = 0; k < p.nsplit; ++k) m = fmaxf(m, cluster.map_shared_rank(sMlC, k)[r].x);
@@ -833,7 +904,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         t.w = fmaf(v.w, f, t.w);
       }
       const float k = kSoftmax ? (l > 0.0f ? 1.0f / l : 0.0f) : inv_n;
-      paged_store<F16>(p, s.q0 + r0 + r, h, c4, make_float4(t.x * k, t.y * k, t.z * k, t.w * k), r < rows);
+      paged_store<F16>(p, s.q0 + r0 + r, h, c4, make_float4(t.x * k, t.y * k, t.z * k, t.w * k), r_of < rows);
     }
   }
   cluster.sync();  // no CTA leaves while another reads its partial sums
