@@ -1007,12 +1007,14 @@ struct PagedJob {
   const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
 };
 
-// Largest power of two of CTAs per cluster (at most 8, the portable size) that
-// still leaves every CTA `min_tiles` key tiles of the longest context, taken only
-// as far as the grid needs it to reach `want` CTAs.
-int paged_splits(int64_t ctas, int64_t want, int max_tiles, int min_tiles) {
+// CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
+// while the grid stays within 1.2 times what the SMs hold at once (`slots`) and the
+// longest context has that many key tiles.  More CTAs than that only add startups:
+// one event over 4096 for 144 (sequence, head) pairs takes 29 us split in 2, 42 us in 3
+// and 39 us in 4; for 240 pairs 38 us whole and 32 us split in 2 (480 CTAs, 444 slots).
+int paged_splits(int64_t ctas, int64_t slots, int max_tiles) {
   int ns = 1;
-  while (ns < 8 && ctas * ns < want && max_tiles >= 2 * ns * min_tiles) ns *= 2;
+  while (ns < 8 && 10 * ctas * ns * 2 <= 12 * slots && 2 * ns <= max_tiles) ns *= 2;
   return ns;
 }
 
@@ -1095,7 +1097,7 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   if (ca->dtype == HSTU_FP32) {
     p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PG32_KEYS), 1);
+    p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PG32_KEYS));
     return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
   }
   const bool f16 = ca->dtype == HSTU_FP16;
@@ -1106,7 +1108,8 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
   p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PGS_KEYS), 1);
+  p.nsplit = paged_splits(ctas, (mh <= 2 ? 3 : 2) * di->sm_count, tiles_of(PGS_KEYS));
+  p.sorted = p.B > 1 && p.B <= 128 && ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
   return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);
 }

@@ -48,6 +48,7 @@ struct PagedParams {
   int32_t max_new, max_context, window, sinks;
   int32_t groups;            // row groups per sequence
   int32_t nsplit;            // CTAs of a cluster
+  int32_t sorted;            // longest sequences first (at most 128 of them)
   uint64_t timeout_ns;
   int32_t thr[MAX_TIME_BUCKETS];  // time-bucket thresholds clamped to int32
   int4 oct[32];
@@ -97,6 +98,28 @@ __device__ __forceinline__ int paged_seq(const PagedParams& p, int u, int r0, in
   s.n_tiles = s.n_sink + (i1 + KEYS - 1) / KEYS - s.first;
   s.n = i1;  // keys past the group's last row are seen by none of its rows
   return 1;
+}
+
+// The sequence of the u-th longest context (ties: the lower index).  The grid starts
+// CTAs in order, so with a few waves of ragged contexts the short ones fill the gaps
+// that the long ones leave.  sLen: 128 ints; every thread of the CTA takes part.
+__device__ __forceinline__ int paged_nth_longest(const PagedParams& p, int u, int32_t* sLen, int* sU) {
+  const int t = threadIdx.x;
+  if (t < p.B) {
+    const int seq = p.seq_ids != nullptr ? p.seq_ids[t] : t;
+    const bool live = static_cast<uint32_t>(seq) < static_cast<uint32_t>(p.num_seqs) &&
+                      p.q_offsets[t + 1] > p.q_offsets[t];
+    sLen[t] = live ? p.lengths[seq] : -1;
+  }
+  __syncthreads();
+  if (t < p.B) {
+    const int mine = sLen[t];
+    int rank = 0;
+    for (int v = 0; v < p.B; ++v) rank += sLen[v] > mine || (sLen[v] == mine && v < t);
+    if (rank == u) *sU = t;
+  }
+  __syncthreads();
+  return *sU;
 }
 
 // Seconds relative to the last event, shifted into [0, 2^31 - 3].
@@ -282,16 +305,16 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 // keys split over a cluster.  Bound
 // by the cache bandwidth, so the tensor work runs on warp-level MMAs (m16n8k16)
 // whose operands and results stay in registers: a 128-row tcgen05 tile would do
-// the element work of 128 rows for the 1..32 that exist.  Warp w of 8 owns keys
-// 16 w .. 16 w + 15 of every 128-key tile for all the rows: S = Q K^T, the element
-// work and O += P V need no exchange between warps until the end.  A ninth warp
+// the element work of 128 rows for the 1..32 that exist.  Warp w of 4 owns keys
+// 16 w .. 16 w + 15 of every 64-key tile for all the rows: S = Q K^T, the element
+// work and O += P V need no exchange between warps until the end.  A fifth warp
 // streams K, V (TMA, one box per page part, 128B swizzle), key times and the
 // position band (cp.async) through a ring of stages, and never waits for a value it
 // loads: block-table entries come 32 boxes at a time, a batch ahead.
-constexpr int PGS_KEYS = 128;  // keys per tile, 16 per warp
-constexpr int PGS_WARPS = 8;
+constexpr int PGS_KEYS = 64;  // keys per tile, 16 per warp
+constexpr int PGS_WARPS = 4;
 constexpr int PGS_THREADS = (PGS_WARPS + 1) * 32;
-constexpr int PGS_STAGES = 3;
+constexpr int PGS_STAGES = 4;
 constexpr uint32_t PGS_TILE_BYTES = PGS_KEYS * 128;
 constexpr int PGS_OLD = 68;  // row stride (floats) of the partial sums: 16-byte rows, no bank conflicts
 
@@ -422,7 +445,7 @@ __device__ __forceinline__ void paged_store(const PagedParams& p, int64_t row, i
 }
 
 template <int PHI, bool F16, int MH>
-__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 3 : 2)
 hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ PagedParams p) {
   constexpr int MT = (MH + 1) / 2;  // 16-row MMA tiles
   constexpr int R = 16 * MT;
@@ -436,7 +459,10 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   const int split = static_cast<int>(blockIdx.x % p.nsplit);
   const int64_t id = blockIdx.x / p.nsplit;
   const int h = static_cast<int>(id % p.H);
-  const int g = static_cast<int>((id / p.H) % p.groups), u = static_cast<int>(id / p.H / p.groups);
+  const int g = static_cast<int>((id / p.H) % p.groups);
+  int u = static_cast<int>(id / p.H / p.groups);
+  if (p.sorted)
+    u = paged_nth_longest(p, u, reinterpret_cast<int32_t*>(smem), reinterpret_cast<int*>(smem + 1024));
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   PagedSeq<PGS_KEYS> s;
   const int r0 = g * R;
@@ -477,7 +503,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
     const int psl = p.ps_log2, ps = 1 << psl;
     const int boxl = min(psl, 6), box = 1 << boxl;  // rows of a box: a page or 64 rows of one
-    const int nbl = 7 - boxl;                       // log2 of the boxes of a tile
+    const int nbl = 6 - boxl;                       // log2 of the boxes of a tile
     const int32_t oob = static_cast<int32_t>((static_cast<int64_t>(p.num_pages) * 2 * p.H) << psl);
     const int per = 32 >> nbl;  // tiles per batch of block-table entries
     const int bx = lane & ((1 << nbl) - 1);
@@ -679,6 +705,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           ldsm_x4(kaddr + soff[t] + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
 #pragma unroll
           for (int a = 0; a < MT; ++a) {
+            if (MT > 1 && 16 * a >= rows) continue;
             if (k == 0) {
               mma_m16n8k16_first<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
               mma_m16n8k16_first<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
@@ -729,6 +756,10 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         }
 #pragma unroll
         for (int a = 0; a < MH; ++a) {
+          if (MH == 4 && 8 * a >= rows) {  // rows of this half do not exist
+            pf[t][a >> 1][(a & 1)] = pf[t][a >> 1][(a & 1) + 2] = 0u;
+            continue;
+          }
           const int r = gr + 8 * a;
           float x[4];
 #pragma unroll
@@ -762,6 +793,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         // rescaled only when some row's maximum grew
 #pragma unroll
         for (int a = 0; a < MH; ++a) {
+          if (MH == 4 && 8 * a >= rows) continue;
           float cm = -INFINITY;
 #pragma unroll
           for (int t = 0; t < N; ++t)
@@ -806,6 +838,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           ldsm_x4_t(vaddr + soff[t] + (((b + vch) ^ (vrow & 7)) << 4), vf);
 #pragma unroll
           for (int a = 0; a < MT; ++a) {
+            if (MT > 1 && 16 * a >= rows) continue;
             mma_m16n8k16<F16>(o[a][b], pf[t][a], vf[0], vf[1]);
             mma_m16n8k16<F16>(o[a][b + 1], pf[t][a], vf[2], vf[3]);
           }
@@ -840,12 +873,12 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     }
   }
   __syncthreads();
-  // the CTA's sums over its warps, in place of warp 0's (16 rows x 16 lanes a step)
+  // the CTA's sums over its warps, in place of warp 0's (8 rows x 16 lanes a step)
   const bool alone = p.nsplit == 1;
   const int c4 = tid & 15;
   const float inv_n = kSoftmax ? 1.0f : 1.0f / static_cast<float>(n_all);
   if (warp < PGS_WARPS) {
-    for (int r = tid >> 4; r < 8 * MH; r += 16) {
+    for (int r = tid >> 4; r < 8 * MH; r += 8) {
       float f[PGS_WARPS], m = -INFINITY, l = 0.0f;
 #pragma unroll
       for (int w = 0; w < PGS_WARPS; ++w) f[w] = 1.0f;
@@ -883,7 +916,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   if (warp < PGS_WARPS) {
     // rank `split` takes rows split, split + nsplit, .. (16 lanes a row; every lane of a
     // warp goes through the same steps)
-    for (int base = 0; base < 8 * MH; base += 16 * p.nsplit) {
+    for (int base = 0; base < 8 * MH; base += 8 * p.nsplit) {
       const int r_of = base + split + p.nsplit * (tid >> 4);
       const int r = min(r_of, 8 * MH - 1);
       float m = -INFINITY, l = 0.0f;
