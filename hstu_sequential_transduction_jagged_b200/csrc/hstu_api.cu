@@ -248,6 +248,22 @@ PagedRowsFn paged_rows_kernel_ptr(int phi, bool f16, int mh) {
   return f16 ? paged_rows_kernel_halves<true>(phi, mh) : paged_rows_kernel_halves<false>(phi, mh);
 }
 
+using PagedTileFn = void (*)(const CUtensorMap, const CUtensorMap, const PagedParams);
+
+template <bool F16>
+PagedTileFn paged_tile_kernel_for(int phi) {
+  switch (phi) {
+    case HSTU_ACT_SILU: return hstu_paged_tile_kernel<HSTU_ACT_SILU, F16>;
+    case HSTU_ACT_RELU: return hstu_paged_tile_kernel<HSTU_ACT_RELU, F16>;
+    case HSTU_ACT_SOFTMAX: return hstu_paged_tile_kernel<HSTU_ACT_SOFTMAX, F16>;
+    default: return hstu_paged_tile_kernel<HSTU_ACT_IDENTITY, F16>;
+  }
+}
+
+PagedTileFn paged_tile_kernel_ptr(int phi, bool f16) {
+  return f16 ? paged_tile_kernel_for<true>(phi) : paged_tile_kernel_for<false>(phi);
+}
+
 struct DeviceInfo {
   int sm_count = 0;
   bool smem_set = false;
@@ -281,6 +297,11 @@ hstu_status_t device_info(DeviceInfo** out) {
       for (int f16 = 0; f16 < 2; ++f16)
         HSTU_CHECK_CUDA(cudaFuncSetAttribute(attn_bwd_kernel_ptr(phi, f16 != 0),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, att_max));
+    for (int phi = 0; phi < 4; ++phi)
+      for (int f16 = 0; f16 < 2; ++f16)
+        HSTU_CHECK_CUDA(cudaFuncSetAttribute(paged_tile_kernel_ptr(phi, f16 != 0),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(PgtSmem::kBytes)));
     for (int phi = 0; phi < 4; ++phi)
       for (int f16 = 0; f16 < 2; ++f16)
         for (int mh = 1; mh <= 4; mh *= 2)
@@ -1007,6 +1028,9 @@ struct PagedJob {
   const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
 };
 
+// Rows per sequence from which the many-rows kernel is taken.
+constexpr int PAGED_TILE_MIN_ROWS = 32;
+
 // CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
 // while the grid stays within 1.2 times what the SMs hold at once (`slots`) and the
 // longest context has that many key tiles.  More CTAs than that only add startups:
@@ -1105,6 +1129,16 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
   if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, 64), f16)) != HSTU_OK)
     return s;
+  if (max_new > PAGED_TILE_MIN_ROWS) {
+    CUtensorMap mq;
+    const int64_t hc = static_cast<int64_t>(p.H) * 64;
+    if ((s = make_map_16(&mq, q, p.T, hc, ldq, 64, 128, f16)) != HSTU_OK) return s;
+    p.groups = (max_new + PGT_ROWS - 1) / PGT_ROWS;
+    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
+    p.nsplit = paged_splits(ctas, di->sm_count, tiles_of(PGT_KEYS));
+    return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), ctas, p.nsplit, PGT_THREADS, PgtSmem::kBytes, st,
+                          mq, mkv, p);
+  }
   const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
   p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;

@@ -943,4 +943,573 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   cluster.sync();  // no CTA leaves while another reads its partial sums
 }
 
+// ---------------------------------------------------------------- many rows
+
+// 16-bit operands, 256 query rows per CTA (two 128-row tcgen05 tiles), keys split
+// over a cluster.  Bound by the element work, one pre-activation, bias and phi2 per
+// (row, key): the layout is hstu_attn_kernel's (16 element warps in two groups of
+// two warpgroups, a producer warp, one MMA issuer per query tile; S in three
+// tensor-memory buffers per tile, P written back over S, O += P V from tensor
+// memory), fed from pages: K and V by TMA boxes, key times and the tile's band of
+// position biases by bulk copies, so that one stage carries all that its 64 keys
+// need and no per-sequence table is staged.  Both tiles walk the whole list of key
+// tiles (the earlier rows waste at most the two that only later rows see).
+// Softmax takes two passes, the first for each row's maximum and sum.
+constexpr int PGT_KEYS = 64;
+constexpr int PGT_ROWS = 256;
+constexpr int PGT_STAGES = 6;
+constexpr int PGT_SBUF = 3;
+constexpr int PGT_THREADS = 608;
+constexpr int PGT_PRODUCER = 16;
+constexpr int PGT_MMA = 17;  // + query tile
+constexpr uint32_t PGT_TILE_BYTES = PGT_KEYS * 128;
+constexpr int PGT_BAND = PGT_KEYS + PGT_ROWS + 4;
+constexpr int PGT_OLD = 68;
+
+struct PgtSmem {
+  static constexpr uint32_t kQ = 0;                                   // 2 x 16 KB
+  static constexpr uint32_t kK = kQ + 2 * 128 * 128;
+  static constexpr uint32_t kV = kK + PGT_STAGES * PGT_TILE_BYTES;
+  static constexpr uint32_t kSide = kV + PGT_STAGES * PGT_TILE_BYTES;  // per stage: times, biases
+  static constexpr uint32_t kSideBytes = PGT_KEYS * 8 + PGT_BAND * 4;
+  static constexpr uint32_t kTime = kSide + PGT_STAGES * kSideBytes;
+  static constexpr uint32_t kThr = kTime + MAX_TIME_BUCKETS * 4;
+  static constexpr uint32_t kOct = kThr + MAX_TIME_BUCKETS * 4;
+  static constexpr uint32_t kOrt = kOct + 32 * 16;
+  static constexpr uint32_t kMl = kOrt + 32 * 16;                      // 2 halves x 256 rows float2
+  static constexpr uint32_t kMlC = kMl + 2 * PGT_ROWS * 8;             // 256 rows float2
+  static constexpr uint32_t kBars = kMlC + PGT_ROWS * 8;
+  static constexpr uint32_t kMisc = kBars + 48 * 8;
+  static constexpr uint32_t kBytes = kMisc + 64 + 1024;                // + align slack
+  static_assert(kSideBytes % 16 == 0 && kSide % 16 == 0, "bulk copies");
+  static_assert(PGT_ROWS * PGT_OLD * 4 <= kSide, "the partial sums fit over Q, K and V");
+};
+
+enum : int {
+  PGB_Q = 0,
+  PGB_FULL = 1,                             // + stage
+  PGB_EMPTY = PGB_FULL + PGT_STAGES,        // + stage
+  PGB_S = PGB_EMPTY + PGT_STAGES,           // + PGT_SBUF * tile + buffer
+  PGB_P = PGB_S + 2 * PGT_SBUF,             // + PGT_SBUF * tile + buffer
+  PGB_DONE = PGB_P + 2 * PGT_SBUF,          // + tile: every MMA of the tile completed
+  PGB_TAIL = PGB_DONE + 2,                  // the loads of a tile that is cleaned before use
+  PGB_COUNT = PGB_TAIL + 1
+};
+static_assert(PGB_COUNT <= 48, "barrier slots");
+
+// Pre-activations h = scale * (s + rab_pos) + scale * rab_time of one row and 32
+// keys, handed to sink(c, h2) in pairs (c even).  bp[-c]: the bias of column c; kts:
+// the keys' times.  `w`: the row's bucket and the latest time still in it.
+struct PagedWalk {
+  int32_t ti;      // the row's time, paged_rel
+  int b;           // bucket of the last key looked up
+  int64_t bound;   // keys up to this time are still in it
+  float rt;
+};
+template <class Sink>
+__device__ __forceinline__ void paged_chunk(const uint32_t (&sv)[32], Sink&& sink, const float* bp,
+                                            const int64_t* kts, bool ragged, bool live, PagedWalk& w,
+                                            int64_t t_last, const float* sTime, const int32_t* sThr,
+                                            const int4* sOct, const float4* sOrt, uint64_t scale2) {
+  const unsigned all = 0xffffffffu;
+  auto pre = [&](int c, uint64_t rt2) -> uint64_t {
+    const uint64_t s2 = f2_pack(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+    return f2_fma(f2_add(s2, f2_pack(bp[-c], bp[-c - 1])), scale2, rt2);
+  };
+  const int64_t t_end = kts[31];
+  // every row's bucket holds to the last key
+  if (!ragged && __all_sync(all, !live || t_end <= w.bound)) {
+    if (live) {
+      const uint64_t rt2 = f2_pack(w.rt, w.rt);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) sink(c, pre(c, rt2));
+    }
+    return;
+  }
+  const int64_t t0 = kts[0];
+  const int b0 = t0 <= w.bound ? w.b : time_bucket_octave(w.ti - paged_rel(t0, t_last), sOct);
+  const int b1 = t_end <= w.bound ? w.b : time_bucket_octave(w.ti - paged_rel(t_end, t_last), sOct);
+  auto edge_of = [&](int b) -> int64_t { return b == 0 ? INT64_MAX : t_last - PG_T0 + (w.ti - sThr[b]); };
+  if (!ragged && __all_sync(all, !live || b0 - b1 <= 1)) {
+    // at most two buckets in a row: keys up to the first one's edge, and the others
+    if (live) {
+      const float hi = sTime[b0], lo = sTime[b1];
+      const int64_t edge = b0 == b1 ? INT64_MAX : edge_of(b0);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2)
+        sink(c, pre(c, f2_pack(kts[c] <= edge ? hi : lo, kts[c + 1] <= edge ? hi : lo)));
+    }
+  } else if (live) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 2)
+      sink(c, pre(c, f2_pack(time_bias_octave(w.ti - paged_rel(kts[c], t_last), sOct, sOrt),
+                             time_bias_octave(w.ti - paged_rel(kts[c + 1], t_last), sOct, sOrt))));
+  }
+  // keys that no row sees have no time: the next chunk looks its buckets up
+  w.b = b1;
+  w.rt = sTime[b1];
+  w.bound = ragged ? INT64_MIN : edge_of(b1);
+}
+
+template <int PHI, bool F16>
+__global__ void __launch_bounds__(PGT_THREADS, 1)
+hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+                       const __grid_constant__ PagedParams p) {
+  constexpr bool kSoftmax = PHI == HSTU_ACT_SOFTMAX;
+  constexpr int kPasses = kSoftmax ? 2 : 1;
+  constexpr float kScale = phi_scale<PHI>();
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  namespace cg = cooperative_groups;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int split = static_cast<int>(blockIdx.x % p.nsplit);
+  const int64_t id = blockIdx.x / p.nsplit;
+  const int h = static_cast<int>(id % p.H);
+  // later rows see more keys: first
+  const int g = p.groups - 1 - static_cast<int>((id / p.H) % p.groups);
+  const int u = static_cast<int>(id / p.H / p.groups);
+  const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
+  PagedSeq<PGT_KEYS> s;
+  const int r0 = g * PGT_ROWS;
+  const int go = paged_seq(p, u, r0, PGT_ROWS, s);
+  if (go <= 0) {  // the same for the whole cluster, before any barrier or allocation
+    if (go < 0 && tid == 0) record_status(HSTU_ERR_DEVICE_CHECK);
+    return;
+  }
+  const int rows = min(PGT_ROWS, s.c - r0);
+  const bool has_b = rows > 128;
+  const int n_all = p.lengths[s.seq];
+  const int i0 = n_all - s.c + r0;
+  const int64_t t_last = p.q_ts[s.q0 + s.c - 1];
+  const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
+  const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
+  const int n_k = k_end - k_begin;      // key tiles of this CTA
+  const int n_items = kPasses * n_k;    // stages it goes through
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PgtSmem::kBars);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + PgtSmem::kMisc);
+  volatile int* sAbort = reinterpret_cast<volatile int*>(smem + PgtSmem::kMisc + 4);
+  float* sTime = reinterpret_cast<float*>(smem + PgtSmem::kTime);
+  int32_t* sThr = reinterpret_cast<int32_t*>(smem + PgtSmem::kThr);
+  int4* sOct = reinterpret_cast<int4*>(smem + PgtSmem::kOct);
+  float4* sOrt = reinterpret_cast<float4*>(smem + PgtSmem::kOrt);
+  float2* sMl = reinterpret_cast<float2*>(smem + PgtSmem::kMl);
+  float2* sMlC = reinterpret_cast<float2*>(smem + PgtSmem::kMlC);
+  if (tid == 0) {
+    mbar_init(&bars[PGB_Q], 1);
+    for (int k = 0; k < PGT_STAGES; ++k) {
+      mbar_init(&bars[PGB_FULL + k], 1 + 32);  // the expect-tx arrival, the producer lanes' copies
+      mbar_init(&bars[PGB_EMPTY + k], 2);      // one commit per issuer
+    }
+    for (int k = 0; k < 2 * PGT_SBUF; ++k) {
+      mbar_init(&bars[PGB_S + k], 1);
+      mbar_init(&bars[PGB_P + k], 256);
+    }
+    mbar_init(&bars[PGB_DONE], 1);
+    mbar_init(&bars[PGB_DONE + 1], 1);
+    mbar_init(&bars[PGB_TAIL], 1);
+    *sAbort = 0;
+    fence_mbar_init();
+  }
+  if (warp == PGT_MMA) {
+    tmem_alloc(sTmem, 512);
+    tmem_relinquish();
+  }
+  const float* rt_g = p.rab_time + static_cast<int64_t>(h) * p.Tb;
+  for (int k = tid; k < p.Tb; k += PGT_THREADS) {
+    sTime[k] = kScale * __ldg(rt_g + k);
+    sThr[k] = p.thr[k];
+  }
+  if (tid < 32) {
+    const int4 o4 = p.oct[tid];
+    auto tb = [&](int b) { return kScale * __ldg(rt_g + min(max(b, 0), p.Tb - 1)); };
+    sOct[tid] = o4;
+    sOrt[tid] = make_float4(tb(o4.w), tb(o4.w + 1), tb(o4.w + 2), tb(o4.w + 3));
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sTmem;
+  const WaitCtl ctl{sAbort, p.timeout_ns};
+
+  if (warp == PGT_PRODUCER) {
+    // ---------------- producer (the few-rows kernel's, with two more cares: pass 0 of the
+    // softmax leaves V out, and V rows that no row sees are cleared before the MMAs read them)
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bars[PGB_Q], (has_b ? 2 : 1) * 128 * 128);
+      const int32_t qrow = static_cast<int32_t>(s.q0 + r0);
+      tma_load_2d(smem + PgtSmem::kQ, &tm_q, &bars[PGB_Q], h * 64, qrow);
+      if (has_b) tma_load_2d(smem + PgtSmem::kQ + 128 * 128, &tm_q, &bars[PGB_Q], h * 64, qrow + 128);
+    }
+    const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
+    const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
+    const int psl = p.ps_log2, ps = 1 << psl;
+    const int boxl = min(psl, 6), box = 1 << boxl, nbl = 6 - boxl;
+    const int32_t oob = static_cast<int32_t>((static_cast<int64_t>(p.num_pages) * 2 * p.H) << psl);
+    const int per = 32 >> nbl, bx = lane & ((1 << nbl) - 1);
+    const bool rp16 = (reinterpret_cast<uintptr_t>(rp) & 15u) == 0;
+    const uint32_t sbase = smem_u32(smem);
+    int st = 0, issued = 0, tails = 0;
+    uint32_t ph = 1;
+    bool ok_all = true;
+    for (int pass = 0; pass < kPasses && ok_all; ++pass) {
+      const bool with_v = pass == kPasses - 1;
+      auto load_page = [&](int k0, int& j) -> int {
+        const int kk = k0 + (lane >> nbl);
+        if (kk >= k_end) return -1;
+        j = s.tile(kk) * PGT_KEYS + (bx << boxl);
+        if (j >= s.n || (j >= s.sink_end && j + box <= s.lo)) return -1;
+        const int page = tab[j >> psl];
+        return page < 0 ? INT32_MAX : page;  // seen, and no page
+      };
+      int j_cur = 0, j_next = 0;
+      int cur = load_page(k_begin, j_cur);
+      for (int kb = k_begin; kb < k_end && ok_all; kb += per) {
+        const int next = load_page(kb + per, j_next);
+        int32_t row_k = oob, row_v = oob, ts0 = -1;
+        if (cur >= 0) {
+          if (cur < p.num_pages) {
+            const int32_t slot = j_cur & (ps - 1);
+            row_k = ((cur * 2 * p.H + h) << psl) + slot;
+            row_v = row_k + (p.H << psl);
+            ts0 = (cur << psl) + slot;
+          } else {
+            record_status(HSTU_ERR_DEVICE_CHECK);
+          }
+        }
+        const unsigned with_ts = __ballot_sync(0xffffffffu, ts0 >= 0);
+        const int n_here = min(per, k_end - kb);
+        for (int t = 0; t < n_here; ++t) {
+          const int j0 = s.tile(kb + t) * PGT_KEYS;
+          const int d4 = paged_band0(i0 - j0, PGT_KEYS);
+          const bool bulk = rp16 && d4 >= 0 && d4 + PGT_BAND <= p.P;
+          // keys that no row sees: their slots may hold anything, and 0 times a NaN is a NaN
+          const bool clean = with_v && (j0 + PGT_KEYS > s.n || (j0 < s.lo && j0 + PGT_KEYS > s.sink_end));
+          uint64_t* full = &bars[PGB_FULL + st];
+          uint64_t* land = clean ? &bars[PGB_TAIL] : full;
+          int ok = 0;
+          if (lane == 0) {
+            ok = mbar_wait(&bars[PGB_EMPTY + st], ph, ctl) ? 1 : 0;
+            if (ok) {
+              const unsigned mine = (with_ts >> (t << nbl)) & ((1u << (1 << nbl)) - 1u);
+              mbar_arrive_expect_tx(land, (with_v ? 2 : 1) * PGT_TILE_BYTES + (__popc(mine) << (boxl + 3)) +
+                                              (bulk ? PGT_BAND * 4 : 0));
+            }
+          }
+          if (!__shfl_sync(0xffffffffu, ok, 0)) {
+            ok_all = false;
+            break;
+          }
+          const uint32_t side = sbase + PgtSmem::kSide + st * PgtSmem::kSideBytes;
+          if ((lane >> nbl) == t) {
+            const uint32_t dst = sbase + PgtSmem::kK + st * PGT_TILE_BYTES + (bx << boxl) * 128;
+            tma_load_2d_to(dst, &tm_kv, land, 0, row_k);
+            if (with_v) tma_load_2d_to(dst + (PgtSmem::kV - PgtSmem::kK), &tm_kv, land, 0, row_v);
+            if (ts0 >= 0) bulk_load(side + (bx << (boxl + 3)), p.ts + ts0, 8u << boxl, land);
+          }
+          const uint32_t band = side + PGT_KEYS * 8;
+          if (bulk) {
+            if (lane == 0) bulk_load(band, rp + d4, PGT_BAND * 4, land);
+          } else {
+            for (int y = lane; y < PGT_BAND; y += 32) cp_async4(band + 4 * y, rp + min(max(d4 + y, 0), p.P - 1));
+          }
+          if (clean) {
+            // (a failed wait has raised the abort flag, which ends the other warps' waits)
+            const bool landed = mbar_wait(&bars[PGB_TAIL], static_cast<uint32_t>(tails) & 1u, ctl);
+            ++tails;
+            if (__all_sync(0xffffffffu, landed)) {
+              uint8_t* v = smem + PgtSmem::kV + st * PGT_TILE_BYTES;
+              for (int e = lane; e < PGT_KEYS * 8; e += 32)
+                if (!s.seen(j0 + (e >> 3)))
+                  *reinterpret_cast<uint4*>(v + (e >> 3) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+          }
+          cp_async_arrive(full);
+          ++issued;
+          if (++st == PGT_STAGES) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        cur = next;
+        j_cur = j_next;
+      }
+    }
+    // every issued load lands before shared memory is reused or released
+    if (lane == 0) {
+      mbar_wait_drain(&bars[PGB_Q], 0, p.timeout_ns);
+      for (int k = max(0, issued - PGT_STAGES); k < issued; ++k)
+        mbar_wait_drain(&bars[PGB_FULL + k % PGT_STAGES], (k / PGT_STAGES) & 1, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp >= PGT_MMA) {
+    // ---------------- MMA issuers
+    const int t = warp - PGT_MMA;
+    const bool leader = elect_one();
+    constexpr uint32_t idesc_qk = idesc_16_f32(128, PGT_KEYS, false, false, F16);
+    constexpr uint32_t idesc_pv = idesc_16_f32(128, 64, false, true, F16);
+    const uint32_t tS = tmem + static_cast<uint32_t>(t * PGT_SBUF * 64);
+    const uint32_t tO = tmem + static_cast<uint32_t>(2 * PGT_SBUF * 64 + t * 64);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem + PgtSmem::kQ + t * 128 * 128), 16, 1024);
+    const uint64_t dK0 = smem_desc_sw128(smem_u32(smem + PgtSmem::kK), 16, 1024);
+    const uint64_t dV0 = smem_desc_sw128(smem_u32(smem + PgtSmem::kV), 8192, 1024);
+    constexpr uint64_t kStageDesc = PGT_TILE_BYTES >> 4;
+    auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, par, ctl));
+    };
+    const bool live = t == 0 || has_b;
+    bool ok = !live || wait_all(&bars[PGB_Q], 0);
+    tc_fence_after();
+    int ready = 0;  // stages this warp has seen land
+    auto await_kv = [&](int it) -> bool {
+      while (ready <= it) {
+        if (!wait_all(&bars[PGB_FULL + ready % PGT_STAGES], static_cast<uint32_t>(ready / PGT_STAGES) & 1u))
+          return false;
+        tc_fence_after();
+        ++ready;
+      }
+      return true;
+    };
+    auto issue_s = [&](int it, int b) {
+      const uint64_t dk = dK0 + static_cast<uint64_t>(it % PGT_STAGES) * kStageDesc;
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_bf16_ss(tS + static_cast<uint32_t>(b * 64), dQ + 2 * k, dk + 2 * k, idesc_qk, k > 0 ? 1u : 0u);
+        mma_commit(&bars[PGB_S + PGT_SBUF * t + b]);
+      }
+      __syncwarp();
+    };
+    if (live)
+      for (int it = 0; ok && it < PGT_SBUF && it < n_items; ++it) {
+        ok = await_kv(it);
+        if (ok) issue_s(it, it);
+      }
+    int b = 0;
+    uint32_t ph = 0;
+    for (int it = 0; ok && it < n_items; ++it) {
+      if (live) {
+        ok = wait_all(&bars[PGB_P + PGT_SBUF * t + b], ph);
+        if (!ok) break;
+        tc_fence_after();
+        const int first = (kPasses - 1) * n_k;  // O accumulates over the last pass
+        if (it >= first && leader) {
+          const uint64_t dv = dV0 + static_cast<uint64_t>(it % PGT_STAGES) * kStageDesc;
+          const uint32_t a = tS + static_cast<uint32_t>(b * 64);
+          // P of keys 0-31 sits at columns 0-15 of the buffer, of keys 32-63 at 32-47
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ts(tO, a + (k >> 1) * 32 + (k & 1) * 8, dv + 128 * k, idesc_pv, it > first || k > 0 ? 1u : 0u);
+        }
+        __syncwarp();
+        if (it + PGT_SBUF < n_items) {
+          ok = await_kv(it + PGT_SBUF);
+          if (!ok) break;
+          issue_s(it + PGT_SBUF, b);  // over the P that the MMAs above read
+        }
+        if (++b == PGT_SBUF) {
+          b = 0;
+          ph ^= 1u;
+        }
+      } else {
+        ok = await_kv(it);  // no rows: only keeps the stages' counts
+        if (!ok) break;
+      }
+      if (leader) mma_commit(&bars[PGB_EMPTY + it % PGT_STAGES]);
+      __syncwarp();
+    }
+    if (leader) mma_commit(&bars[PGB_DONE + t]);
+    __syncwarp();
+    mbar_wait_drain(&bars[PGB_DONE + t], 0, p.timeout_ns);
+    __syncwarp();
+  } else {
+    // ---------------- element groups: rows 128 t .. of the group, key columns 32 half ..
+    const int t = warp >> 3, half = (warp >> 2) & 1, r = t * 128 + (tid & 127);
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS0 = tmem + lane_off + static_cast<uint32_t>(t * PGT_SBUF * 64 + half * 32);
+    const uint32_t tO = tmem + lane_off + static_cast<uint32_t>(2 * PGT_SBUF * 64 + t * 64 + half * 32);
+    const bool valid = r < rows;
+    const int i = i0 + r;
+    const uint64_t scale2 = f2_pack(kScale, kScale);
+    PagedWalk w;
+    w.ti = valid ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
+    auto walk_reset = [&]() {
+      w.b = 0;
+      w.bound = INT64_MIN;
+      w.rt = 0.0f;
+    };
+    walk_reset();
+    const bool live = t == 0 || has_b;
+    bool ok = true;
+    float m = -INFINITY, l = 0.0f;  // softmax: this half's maximum and sum
+    int buf = 0;
+    uint32_t ph = 0;
+    auto run_pass = [&](int pass) {
+      for (int k = 0; k < n_k; ++k) {
+        const int it = pass * n_k + k, st = it % PGT_STAGES;
+        ok = mbar_wait(&bars[PGB_S + PGT_SBUF * t + buf], ph, ctl);
+        if (ok) ok = mbar_wait(&bars[PGB_FULL + st], static_cast<uint32_t>(it / PGT_STAGES) & 1u, ctl);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_fence_after();
+        const int j_tile = s.tile(k_begin + k) * PGT_KEYS, j0 = j_tile + half * 32;
+        const int64_t* kts =
+            reinterpret_cast<const int64_t*>(smem + PgtSmem::kSide + st * PgtSmem::kSideBytes) + half * 32;
+        const float* bp = reinterpret_cast<const float*>(smem + PgtSmem::kSide + st * PgtSmem::kSideBytes + PGT_KEYS * 8) +
+                          (i - j0) - paged_band0(i0 - j_tile, PGT_KEYS);
+        const bool ragged = j0 + 32 > s.n || (j0 < s.lo && j0 + 32 > s.sink_end);
+        if (it == 0 && t == 0 && (warp & 3) == 0 && s.seen(j0 + lane) && t_last - kts[lane] > PG_T0)
+          record_status(HSTU_ERR_DEVICE_CHECK);
+        // visible columns of the row, one bit each
+        uint32_t vis = 0u;
+        if (valid && i >= j0) {
+          vis = i - j0 >= 31 ? 0xffffffffu : (2u << (i - j0)) - 1u;
+          if (p.window > 0) {
+            const int lo = i - p.window + 1 - j0, sk = p.sinks - j0;
+            uint32_t in = lo <= 0 ? 0xffffffffu : (lo >= 32 ? 0u : 0xffffffffu << lo);
+            in |= sk >= 32 ? 0xffffffffu : (sk <= 0 ? 0u : (1u << sk) - 1u);
+            vis &= in;
+          }
+        }
+        const bool whole = __all_sync(0xffffffffu, vis == 0xffffffffu);
+        const bool row_live = vis != 0u;
+        uint32_t sv[32];
+        const uint32_t tS = tS0 + static_cast<uint32_t>(buf * 64);
+        tmem_ld32(tS, sv);
+        tmem_ld_wait(sv);
+        uint32_t pk[16];
+        if constexpr (!kSoftmax) {
+          paged_chunk(sv, [&](int c, uint64_t h2) { pk[c >> 1] = phi_pair<PHI, F16>(h2); }, bp, kts, ragged,
+                      row_live, w, t_last, sTime, sThr, sOct, sOrt, scale2);
+        } else {
+          uint64_t hh[16];
+          paged_chunk(sv, [&](int c, uint64_t h2) { hh[c >> 1] = h2; }, bp, kts, ragged, row_live, w, t_last, sTime,
+                      sThr, sOct, sOrt, scale2);
+          float x[32];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            f2_unpack(hh[c >> 1], x[c], x[c + 1]);
+            if (!whole) {
+              x[c] = (vis >> c) & 1u ? x[c] : -INFINITY;
+              x[c + 1] = (vis >> (c + 1)) & 1u ? x[c + 1] : -INFINITY;
+            }
+          }
+          if (pass == 0) {
+            float cm = x[0];
+#pragma unroll
+            for (int c = 1; c < 32; ++c) cm = fmaxf(cm, x[c]);
+            if (row_live && cm > m) {
+              l *= ex2_approx(m - cm);
+              m = cm;
+            }
+            float a0 = 0.0f, a1 = 0.0f;
+            const float mm = m > -INFINITY ? m : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              a0 += ex2_approx(x[c] - mm);
+              a1 += ex2_approx(x[c + 1] - mm);
+            }
+            if (row_live) l += a0 + a1;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) pk[c >> 1] = pack_16<F16>(ex2_approx(x[c] - m), ex2_approx(x[c + 1] - m));
+          }
+        }
+        if (!kSoftmax || pass == 1) {
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const uint32_t keep = ((vis >> c) & 1u ? 0xffffu : 0u) | ((vis >> (c + 1)) & 1u ? 0xffff0000u : 0u);
+              pk[c >> 1] = row_live ? pk[c >> 1] & keep : 0u;
+            }
+          }
+          __syncwarp();
+          tmem_st16(tS, pk);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[PGB_P + PGT_SBUF * t + buf]);
+        if (++buf == PGT_SBUF) {
+          buf = 0;
+          ph ^= 1u;
+        }
+      }
+    };
+    if (live) run_pass(0);
+    if constexpr (kSoftmax) {
+      // P = 2^(x - m) with the row's maximum over both halves; the sum goes with O
+      sMl[half * PGT_ROWS + r] = make_float2(m, l);
+      named_barrier_sync(1 + t, 256);
+      const float2 other = sMl[(half ^ 1) * PGT_ROWS + r];
+      const float mm = fmaxf(m, other.x);
+      if (mm > -INFINITY) l = l * ex2_approx(m - mm) + other.y * ex2_approx(other.x - mm);
+      m = mm > -INFINITY ? mm : 0.0f;
+      if (half == 0) sMlC[r] = make_float2(mm, l);
+      walk_reset();
+      if (live && ok) run_pass(1);
+    }
+    // O to shared memory, once every MMA and load of the CTA is done with it
+    // (with no key tile too: the issuers have then seen Q land)
+    if (ok) ok = mbar_wait(&bars[PGB_DONE], 0, ctl) && mbar_wait(&bars[PGB_DONE + 1], 0, ctl);
+    ok = __all_sync(0xffffffffu, ok);
+    tc_fence_after();
+    named_barrier_sync(3, 512);
+    float* sO = reinterpret_cast<float*>(smem);
+    uint32_t ov[32];
+    if (ok && live && n_k > 0) {
+      tmem_ld32(tO, ov);
+      tmem_ld_wait(ov);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) ov[c] = 0u;
+    }
+    if (live)
+#pragma unroll
+      for (int c = 0; c < 32; c += 4)
+        *reinterpret_cast<uint4*>(sO + r * PGT_OLD + half * 32 + c) = make_uint4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == PGT_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  // ---------------- the sums over the cluster, 16 lanes a row
+  float* sO = reinterpret_cast<float*>(smem);
+  const float inv_n = kSoftmax ? 1.0f : 1.0f / static_cast<float>(n_all);
+  cg::cluster_group cluster = cg::this_cluster();
+  if (p.nsplit > 1) cluster.sync();
+  if (warp < 16) {
+    const int c4 = tid & 15, rr = has_b ? PGT_ROWS : 128;
+    for (int base = 0; base < rr; base += 32 * p.nsplit) {
+      const int r_of = base + split + p.nsplit * (tid >> 4);
+      const int r = min(r_of, rr - 1);
+      float m = -INFINITY, l = 0.0f;
+      if constexpr (kSoftmax)
+        for (int k = 0; k < p.nsplit; ++k)
+          m = fmaxf(m, (p.nsplit > 1 ? cluster.map_shared_rank(sMlC, k) : sMlC)[r].x);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k = 0; k < p.nsplit; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(
+            (p.nsplit > 1 ? cluster.map_shared_rank(sO, k) : sO) + r * PGT_OLD + 4 * c4);
+        float f = 1.0f;
+        if constexpr (kSoftmax) {
+          const float2 ml = (p.nsplit > 1 ? cluster.map_shared_rank(sMlC, k) : sMlC)[r];
+          f = ml.x > -INFINITY ? ex2_approx(ml.x - m) : 0.0f;
+          l = fmaf(ml.y, f, l);
+        }
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+      }
+      const float k = kSoftmax ? (l > 0.0f ? 1.0f / l : 0.0f) : inv_n;
+      paged_store<F16>(p, s.q0 + r0 + r, h, c4, make_float4(o.x * k, o.y * k, o.z * k, o.w * k), r_of < rows);
+    }
+  }
+  if (p.nsplit > 1) cluster.sync();  // no CTA leaves while another reads its partial sums
+}
+
 }  // namespace hstu
