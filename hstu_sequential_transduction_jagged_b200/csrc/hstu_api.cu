@@ -1029,7 +1029,7 @@ struct PagedJob {
 };
 
 // Rows per sequence from which the many-rows kernel is taken.
-constexpr int PAGED_TILE_MIN_ROWS = 32;
+int paged_tile_min_rows(int phi2) { return phi2 == HSTU_ACT_SOFTMAX ? 64 : 32; }
 
 // CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
 // while the grid stays within 1.2 times what the SMs hold at once (`slots`) and the
@@ -1129,7 +1129,7 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
   if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, 64), f16)) != HSTU_OK)
     return s;
-  if (max_new > PAGED_TILE_MIN_ROWS) {
+  if (max_new > paged_tile_min_rows(c->phi2)) {
     CUtensorMap mq;
     const int64_t hc = static_cast<int64_t>(p.H) * 64;
     if ((s = make_map_16(&mq, q, p.T, hc, ldq, 64, 128, f16)) != HSTU_OK) return s;

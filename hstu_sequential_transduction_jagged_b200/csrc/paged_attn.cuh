@@ -953,7 +953,9 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
 // memory), fed from pages: K and V by TMA boxes, key times and the tile's band of
 // position biases by bulk copies, so that one stage carries all that its 64 keys
 // need and no per-sequence table is staged.  Both tiles walk the whole list of key
-// tiles (the earlier rows waste at most the two that only later rows see).
+// tiles (the earlier rows waste at most the two that only later rows see).  A group of
+// at most 128 rows has no second tile: then both halves of the machinery take the
+// same rows and every other key tile each, and their results are added at the end.
 // Softmax takes two passes, the first for each row's maximum and sum.
 constexpr int PGT_KEYS = 64;
 constexpr int PGT_ROWS = 256;
@@ -1076,7 +1078,7 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     return;
   }
   const int rows = min(PGT_ROWS, s.c - r0);
-  const bool has_b = rows > 128;
+  const bool dual = rows <= 128;  // one query tile: key tiles alternate between the groups
   const int n_all = p.lengths[s.seq];
   const int i0 = n_all - s.c + r0;
   const int64_t t_last = p.q_ts[s.q0 + s.c - 1];
@@ -1084,6 +1086,14 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
   const int n_k = k_end - k_begin;      // key tiles of this CTA
   const int n_items = kPasses * n_k;    // stages it goes through
+  // key tile k of the CTA is group t's; each of its passes has own_k of them
+  auto mine = [&](int k, int t) { return !dual || (k & 1) == t; };
+  auto own_k = [&](int t) { return dual ? (n_k + 1 - t) >> 1 : n_k; };
+  // stage of the gi-th item of group t (its tiles, once per pass)
+  auto stage_of = [&](int gi, int t) {
+    const int nk = own_k(t), pass = gi >= nk ? 1 : 0, k = gi - pass * nk;
+    return pass * n_k + (dual ? 2 * k + t : k);
+  };
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + PgtSmem::kBars);
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + PgtSmem::kMisc);
@@ -1135,10 +1145,10 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     // ---------------- producer (the few-rows kernel's, with two more cares: pass 0 of the
     // softmax leaves V out, and V rows that no row sees are cleared before the MMAs read them)
     if (lane == 0) {
-      mbar_arrive_expect_tx(&bars[PGB_Q], (has_b ? 2 : 1) * 128 * 128);
+      mbar_arrive_expect_tx(&bars[PGB_Q], (dual ? 1 : 2) * 128 * 128);
       const int32_t qrow = static_cast<int32_t>(s.q0 + r0);
       tma_load_2d(smem + PgtSmem::kQ, &tm_q, &bars[PGB_Q], h * 64, qrow);
-      if (has_b) tma_load_2d(smem + PgtSmem::kQ + 128 * 128, &tm_q, &bars[PGB_Q], h * 64, qrow + 128);
+      if (!dual) tma_load_2d(smem + PgtSmem::kQ + 128 * 128, &tm_q, &bars[PGB_Q], h * 64, qrow + 128);
     }
     const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
     const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
@@ -1252,15 +1262,14 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     constexpr uint32_t idesc_pv = idesc_16_f32(128, 64, false, true, F16);
     const uint32_t tS = tmem + static_cast<uint32_t>(t * PGT_SBUF * 64);
     const uint32_t tO = tmem + static_cast<uint32_t>(2 * PGT_SBUF * 64 + t * 64);
-    const uint64_t dQ = smem_desc_sw128(smem_u32(smem + PgtSmem::kQ + t * 128 * 128), 16, 1024);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem + PgtSmem::kQ + (dual ? 0 : t * 128 * 128)), 16, 1024);
     const uint64_t dK0 = smem_desc_sw128(smem_u32(smem + PgtSmem::kK), 16, 1024);
     const uint64_t dV0 = smem_desc_sw128(smem_u32(smem + PgtSmem::kV), 8192, 1024);
     constexpr uint64_t kStageDesc = PGT_TILE_BYTES >> 4;
     auto wait_all = [&](uint64_t* bar, uint32_t par) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, par, ctl));
     };
-    const bool live = t == 0 || has_b;
-    bool ok = !live || wait_all(&bars[PGB_Q], 0);
+    bool ok = wait_all(&bars[PGB_Q], 0);
     tc_fence_after();
     int ready = 0;  // stages this warp has seen land
     auto await_kv = [&](int it) -> bool {
@@ -1282,39 +1291,44 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
       }
       __syncwarp();
     };
-    if (live)
-      for (int it = 0; ok && it < PGT_SBUF && it < n_items; ++it) {
-        ok = await_kv(it);
-        if (ok) issue_s(it, it);
-      }
-    int b = 0;
+    // S of the next items is issued ahead of their turn, as far as the ring of stages
+    // reaches when every other one of them is this group's
+    const int ahead = dual ? 2 : PGT_SBUF;
+    const int own_items = kPasses * own_k(t), first = (kPasses - 1) * own_k(t);  // O: the last pass
+    for (int gi = 0; ok && gi < ahead && gi < own_items; ++gi) {
+      ok = await_kv(stage_of(gi, t));
+      if (ok) issue_s(stage_of(gi, t), gi);
+    }
+    int b = 0, b_next = ahead % PGT_SBUF, gi = 0;
     uint32_t ph = 0;
     for (int it = 0; ok && it < n_items; ++it) {
-      if (live) {
+      if (mine(it >= n_k ? it - n_k : it, t)) {
         ok = wait_all(&bars[PGB_P + PGT_SBUF * t + b], ph);
         if (!ok) break;
         tc_fence_after();
-        const int first = (kPasses - 1) * n_k;  // O accumulates over the last pass
-        if (it >= first && leader) {
+        if (gi >= first && leader) {
           const uint64_t dv = dV0 + static_cast<uint64_t>(it % PGT_STAGES) * kStageDesc;
           const uint32_t a = tS + static_cast<uint32_t>(b * 64);
           // P of keys 0-31 sits at columns 0-15 of the buffer, of keys 32-63 at 32-47
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16_ts(tO, a + (k >> 1) * 32 + (k & 1) * 8, dv + 128 * k, idesc_pv, it > first || k > 0 ? 1u : 0u);
+            mma_bf16_ts(tO, a + (k >> 1) * 32 + (k & 1) * 8, dv + 128 * k, idesc_pv, gi > first || k > 0 ? 1u : 0u);
         }
         __syncwarp();
-        if (it + PGT_SBUF < n_items) {
-          ok = await_kv(it + PGT_SBUF);
+        if (gi + ahead < own_items) {
+          const int nx = stage_of(gi + ahead, t);
+          ok = await_kv(nx);
           if (!ok) break;
-          issue_s(it + PGT_SBUF, b);  // over the P that the MMAs above read
+          issue_s(nx, b_next);  // over a P that the MMAs so far read
         }
+        ++gi;
+        if (++b_next == PGT_SBUF) b_next = 0;
         if (++b == PGT_SBUF) {
           b = 0;
           ph ^= 1u;
         }
       } else {
-        ok = await_kv(it);  // no rows: only keeps the stages' counts
+        ok = await_kv(it);  // the other group's: only keeps the stage's count
         if (!ok) break;
       }
       if (leader) mma_commit(&bars[PGB_EMPTY + it % PGT_STAGES]);
@@ -1326,7 +1340,8 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     __syncwarp();
   } else {
     // ---------------- element groups: rows 128 t .. of the group, key columns 32 half ..
-    const int t = warp >> 3, half = (warp >> 2) & 1, r = t * 128 + (tid & 127);
+    const int t = warp >> 3, half = (warp >> 2) & 1, r = (dual ? 0 : t * 128) + (tid & 127);
+    const int slot = t * 128 + (tid & 127);  // where this group's results of the row go
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS0 = tmem + lane_off + static_cast<uint32_t>(t * PGT_SBUF * 64 + half * 32);
     const uint32_t tO = tmem + lane_off + static_cast<uint32_t>(2 * PGT_SBUF * 64 + t * 64 + half * 32);
@@ -1341,13 +1356,12 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
       w.rt = 0.0f;
     };
     walk_reset();
-    const bool live = t == 0 || has_b;
     bool ok = true;
     float m = -INFINITY, l = 0.0f;  // softmax: this half's maximum and sum
     int buf = 0;
     uint32_t ph = 0;
     auto run_pass = [&](int pass) {
-      for (int k = 0; k < n_k; ++k) {
+      for (int k = dual ? t : 0; k < n_k; k += dual ? 2 : 1) {
         const int it = pass * n_k + k, st = it % PGT_STAGES;
         ok = mbar_wait(&bars[PGB_S + PGT_SBUF * t + buf], ph, ctl);
         if (ok) ok = mbar_wait(&bars[PGB_FULL + st], static_cast<uint32_t>(it / PGT_STAGES) & 1u, ctl);
@@ -1437,18 +1451,18 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
         }
       }
     };
-    if (live) run_pass(0);
+    run_pass(0);
     if constexpr (kSoftmax) {
       // P = 2^(x - m) with the row's maximum over both halves; the sum goes with O
-      sMl[half * PGT_ROWS + r] = make_float2(m, l);
+      sMl[half * PGT_ROWS + slot] = make_float2(m, l);
       named_barrier_sync(1 + t, 256);
-      const float2 other = sMl[(half ^ 1) * PGT_ROWS + r];
+      const float2 other = sMl[(half ^ 1) * PGT_ROWS + slot];
       const float mm = fmaxf(m, other.x);
       if (mm > -INFINITY) l = l * ex2_approx(m - mm) + other.y * ex2_approx(other.x - mm);
       m = mm > -INFINITY ? mm : 0.0f;
-      if (half == 0) sMlC[r] = make_float2(mm, l);
+      if (half == 0) sMlC[slot] = make_float2(mm, l);
       walk_reset();
-      if (live && ok) run_pass(1);
+      if (ok) run_pass(1);
     }
     // O to shared memory, once every MMA and load of the CTA is done with it
     // (with no key tile too: the issuers have then seen Q land)
@@ -1458,17 +1472,17 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     named_barrier_sync(3, 512);
     float* sO = reinterpret_cast<float*>(smem);
     uint32_t ov[32];
-    if (ok && live && n_k > 0) {
+    if (ok && own_k(t) > 0) {
       tmem_ld32(tO, ov);
       tmem_ld_wait(ov);
     } else {
 #pragma unroll
       for (int c = 0; c < 32; ++c) ov[c] = 0u;
     }
-    if (live)
 #pragma unroll
-      for (int c = 0; c < 32; c += 4)
-        *reinterpret_cast<uint4*>(sO + r * PGT_OLD + half * 32 + c) = make_uint4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
+    for (int c = 0; c < 32; c += 4)
+      *reinterpret_cast<uint4*>(sO + slot * PGT_OLD + half * 32 + c) =
+          make_uint4(ov[c], ov[c + 1], ov[c + 2], ov[c + 3]);
     tc_fence_before();
   }
   __syncthreads();
@@ -1482,21 +1496,28 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
   cg::cluster_group cluster = cg::this_cluster();
   if (p.nsplit > 1) cluster.sync();
   if (warp < 16) {
-    const int c4 = tid & 15, rr = has_b ? PGT_ROWS : 128;
+    const int c4 = tid & 15, rr = dual ? 128 : PGT_ROWS;
+    const int parts = dual ? 2 * p.nsplit : p.nsplit;  // partial results of a row
     for (int base = 0; base < rr; base += 32 * p.nsplit) {
       const int r_of = base + split + p.nsplit * (tid >> 4);
       const int r = min(r_of, rr - 1);
+      auto part_o = [&](int k) {
+        const int rank = dual ? k >> 1 : k, row = r + (dual ? (k & 1) * 128 : 0);
+        return (p.nsplit > 1 ? cluster.map_shared_rank(sO, rank) : sO) + row * PGT_OLD + 4 * c4;
+      };
+      auto part_ml = [&](int k) {
+        const int rank = dual ? k >> 1 : k, row = r + (dual ? (k & 1) * 128 : 0);
+        return (p.nsplit > 1 ? cluster.map_shared_rank(sMlC, rank) : sMlC)[row];
+      };
       float m = -INFINITY, l = 0.0f;
       if constexpr (kSoftmax)
-        for (int k = 0; k < p.nsplit; ++k)
-          m = fmaxf(m, (p.nsplit > 1 ? cluster.map_shared_rank(sMlC, k) : sMlC)[r].x);
+        for (int k = 0; k < parts; ++k) m = fmaxf(m, part_ml(k).x);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int k = 0; k < p.nsplit; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(
-            (p.nsplit > 1 ? cluster.map_shared_rank(sO, k) : sO) + r * PGT_OLD + 4 * c4);
+      for (int k = 0; k < parts; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(part_o(k));
         float f = 1.0f;
         if constexpr (kSoftmax) {
-          const float2 ml = (p.nsplit > 1 ? cluster.map_shared_rank(sMlC, k) : sMlC)[r];
+          const float2 ml = part_ml(k);
           f = ml.x > -INFINITY ? ex2_approx(ml.x - m) : 0.0f;
           l = fmaf(ml.y, f, l);
         }
