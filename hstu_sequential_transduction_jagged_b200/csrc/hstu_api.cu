@@ -1117,11 +1117,15 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   int64_t seen = p.max_context;
   if (p.window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(p.window) + max_new + p.sinks);
   auto tiles_of = [&](int keys) { return static_cast<int>((seen + keys - 1) / keys); };
+  // (sequence, head, row group) triples that have rows: at most this many of the grid's
+  auto busy = [&](int rows) {
+    return std::min<int64_t>(static_cast<int64_t>(p.B) * p.groups, p.T / rows + p.B) * p.H;
+  };
   ProfScope prof(K_PAGED_ATTN, st);
   if (ca->dtype == HSTU_FP32) {
     p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(ctas, 2 * di->sm_count, tiles_of(PG32_KEYS));
+    p.nsplit = paged_splits(busy(PG32_ROWS), 4 * di->sm_count, tiles_of(PG32_KEYS));
     return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
   }
   const bool f16 = ca->dtype == HSTU_FP16;
@@ -1135,14 +1139,14 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
     if ((s = make_map_16(&mq, q, p.T, hc, ldq, 64, 128, f16)) != HSTU_OK) return s;
     p.groups = (max_new + PGT_ROWS - 1) / PGT_ROWS;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(ctas, di->sm_count, tiles_of(PGT_KEYS));
+    p.nsplit = paged_splits(busy(PGT_ROWS), di->sm_count, tiles_of(PGT_KEYS));
     return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), ctas, p.nsplit, PGT_THREADS, PgtSmem::kBytes, st,
                           mq, mkv, p);
   }
   const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
   p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(ctas, (mh <= 2 ? 3 : 2) * di->sm_count, tiles_of(PGS_KEYS));
+  p.nsplit = paged_splits(busy(8 * mh), (mh <= 2 ? 3 : 2) * di->sm_count, tiles_of(PGS_KEYS));
   p.sorted = p.B > 1 && p.B <= 128 && ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
   return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);

@@ -789,8 +789,9 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
         }
       }
       if constexpr (kSoftmax) {
-        // running maximum over the step's keys, then P = 2^(x - m); a warp's O is
-        // rescaled only when some row's maximum grew
+        // P = 2^(x - m) with a running m that follows the rows' maxima only when one of them
+        // is more than 8 above it: P stays below 2^8, no sum loses anything, and most
+        // steps need neither the quad's maximum nor a rescaled O
 #pragma unroll
         for (int a = 0; a < MH; ++a) {
           if (MH == 4 && 8 * a >= rows) continue;
@@ -799,9 +800,9 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
           for (int t = 0; t < N; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) cm = fmaxf(cm, sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)]);
-          cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
-          cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
-          if (__any_sync(0xffffffffu, cm > m_run[a])) {
+          if (__any_sync(0xffffffffu, cm > m_run[a] + 8.0f)) {
+            cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
+            cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
             const float mn = fmaxf(m_run[a], cm);
             const float f = mn > -INFINITY ? ex2_approx(m_run[a] - mn) : 1.0f;
             m_run[a] = mn;
@@ -1350,6 +1351,10 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
     const uint64_t scale2 = f2_pack(kScale, kScale);
     PagedWalk w;
     w.ti = valid ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
+    // the CTA's tiles [f_lo, f_hi) that every row of this group's tile sees whole
+    const int t_i0 = i0 + (dual ? 0 : t * 128), t_i1 = i0 + min(rows, (dual ? 0 : t * 128) + 128) - 1;
+    const int f_lo = (p.window == 0 ? 0 : s.n_sink + max(0, (t_i1 - p.window + PGT_KEYS) / PGT_KEYS - s.first)) - k_begin;
+    const int f_hi = s.n_sink + (t_i0 + 1) / PGT_KEYS - s.first - k_begin;
     auto walk_reset = [&]() {
       w.b = 0;
       w.bound = INT64_MIN;
@@ -1373,12 +1378,13 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             reinterpret_cast<const int64_t*>(smem + PgtSmem::kSide + st * PgtSmem::kSideBytes) + half * 32;
         const float* bp = reinterpret_cast<const float*>(smem + PgtSmem::kSide + st * PgtSmem::kSideBytes + PGT_KEYS * 8) +
                           (i - j0) - paged_band0(i0 - j_tile, PGT_KEYS);
-        const bool ragged = j0 + 32 > s.n || (j0 < s.lo && j0 + 32 > s.sink_end);
+        const bool ragged = (k < f_lo || k >= f_hi) && (j0 + 32 > s.n || (j0 < s.lo && j0 + 32 > s.sink_end));
         if (it == 0 && t == 0 && (warp & 3) == 0 && s.seen(j0 + lane) && t_last - kts[lane] > PG_T0)
           record_status(HSTU_ERR_DEVICE_CHECK);
-        // visible columns of the row, one bit each
-        uint32_t vis = 0u;
-        if (valid && i >= j0) {
+        // visible columns of the row, one bit each (inside [f_lo, f_hi) all of them)
+        uint32_t vis = valid ? 0xffffffffu : 0u;
+        if (k < f_lo || k >= f_hi) vis = 0u;
+        if (vis == 0u && valid && i >= j0) {
           vis = i - j0 >= 31 ? 0xffffffffu : (2u << (i - j0)) - 1u;
           if (p.window > 0) {
             const int lo = i - p.window + 1 - j0, sk = p.sinks - j0;
@@ -1387,7 +1393,8 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
             vis &= in;
           }
         }
-        const bool whole = __all_sync(0xffffffffu, vis == 0xffffffffu);
+        // (rows that do not exist are nobody's: their P may be anything)
+        const bool whole = __all_sync(0xffffffffu, vis == 0xffffffffu || !valid);
         const bool row_live = vis != 0u;
         uint32_t sv[32];
         const uint32_t tS = tS0 + static_cast<uint32_t>(buf * 64);
@@ -1398,17 +1405,12 @@ hstu_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_co
           paged_chunk(sv, [&](int c, uint64_t h2) { pk[c >> 1] = phi_pair<PHI, F16>(h2); }, bp, kts, ragged,
                       row_live, w, t_last, sTime, sThr, sOct, sOrt, scale2);
         } else {
-          uint64_t hh[16];
-          paged_chunk(sv, [&](int c, uint64_t h2) { hh[c >> 1] = h2; }, bp, kts, ragged, row_live, w, t_last, sTime,
-                      sThr, sOct, sOrt, scale2);
           float x[32];
+          paged_chunk(sv, [&](int c, uint64_t h2) { f2_unpack(h2, x[c], x[c + 1]); }, bp, kts, ragged, row_live, w,
+                      t_last, sTime, sThr, sOct, sOrt, scale2);
+          if (!whole) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            f2_unpack(hh[c >> 1], x[c], x[c + 1]);
-            if (!whole) {
-              x[c] = (vis >> c) & 1u ? x[c] : -INFINITY;
-              x[c + 1] = (vis >> (c + 1)) & 1u ? x[c + 1] : -INFINITY;
-            }
+            for (int c = 0; c < 32; ++c) x[c] = (vis >> c) & 1u ? x[c] : -INFINITY;
           }
           if (pass == 0) {
             float cm = x[0];
