@@ -238,14 +238,10 @@ PagedRowsFn paged_rows_kernel_for(int phi) {
   }
 }
 
-template <bool F16>
-PagedRowsFn paged_rows_kernel_halves(int phi, int mh) {
-  return mh == 1 ? paged_rows_kernel_for<F16, 1>(phi)
-                 : (mh == 2 ? paged_rows_kernel_for<F16, 2>(phi) : paged_rows_kernel_for<F16, 4>(phi));
-}
-
+// mh: 8-row halves per CTA, 1 or 2
 PagedRowsFn paged_rows_kernel_ptr(int phi, bool f16, int mh) {
-  return f16 ? paged_rows_kernel_halves<true>(phi, mh) : paged_rows_kernel_halves<false>(phi, mh);
+  if (f16) return mh == 1 ? paged_rows_kernel_for<true, 1>(phi) : paged_rows_kernel_for<true, 2>(phi);
+  return mh == 1 ? paged_rows_kernel_for<false, 1>(phi) : paged_rows_kernel_for<false, 2>(phi);
 }
 
 using PagedTileFn = void (*)(const CUtensorMap, const CUtensorMap, const PagedParams);
@@ -304,7 +300,7 @@ hstu_status_t device_info(DeviceInfo** out) {
                                              static_cast<int>(PgtSmem::kBytes)));
     for (int phi = 0; phi < 4; ++phi)
       for (int f16 = 0; f16 < 2; ++f16)
-        for (int mh = 1; mh <= 4; mh *= 2)
+        for (int mh = 1; mh <= 2; ++mh)
           HSTU_CHECK_CUDA(cudaFuncSetAttribute(paged_rows_kernel_ptr(phi, f16 != 0, mh),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(PgsSmem::kBytes)));
@@ -1032,13 +1028,14 @@ struct PagedJob {
 int paged_tile_min_rows(int phi2) { return phi2 == HSTU_ACT_SOFTMAX ? 64 : 32; }
 
 // CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
-// while the grid stays within 1.2 times what the SMs hold at once (`slots`) and the
+// while the grid stays within 1.1 times what the SMs hold at once (`slots`) and the
 // longest context has that many key tiles.  More CTAs than that only add startups:
 // one event over 4096 for 144 (sequence, head) pairs takes 29 us split in 2, 42 us in 3
-// and 39 us in 4; for 240 pairs 38 us whole and 32 us split in 2 (480 CTAs, 444 slots).
+// and 39 us in 4; 16 events for 128 pairs 35 us in 2 and 49 us in 4; one event over
+// 100 .. 4096 for 240 pairs 38 us whole and 32 us in 2 (480 CTAs, 444 slots).
 int paged_splits(int64_t ctas, int64_t slots, int max_tiles) {
   int ns = 1;
-  while (ns < 8 && 10 * ctas * ns * 2 <= 12 * slots && 2 * ns <= max_tiles) ns *= 2;
+  while (ns < 8 && 10 * ctas * ns * 2 <= 11 * slots && 2 * ns <= max_tiles) ns *= 2;
   return ns;
 }
 
@@ -1143,10 +1140,10 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
     return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), ctas, p.nsplit, PGT_THREADS, PgtSmem::kBytes, st,
                           mq, mkv, p);
   }
-  const int mh = max_new <= 8 ? 1 : (max_new <= 16 ? 2 : 4);  // 8-row halves per CTA
+  const int mh = max_new <= 8 ? 1 : 2;
   p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(busy(8 * mh), (mh <= 2 ? 3 : 2) * di->sm_count, tiles_of(PGS_KEYS));
+  p.nsplit = paged_splits(busy(8 * mh), 3 * di->sm_count, tiles_of(PGS_KEYS));
   p.sorted = p.B > 1 && p.B <= 128 && ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
   return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);

@@ -22,8 +22,6 @@
 
 #include <cooperative_groups.h>
 
-#include <type_traits>
-
 #include "attn.cuh"
 
 namespace hstu {
@@ -301,11 +299,11 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 
 // ---------------------------------------------------------------- few rows
 
-// 16-bit operands, 8 * MH query rows per CTA (1, 2 or 4 halves of a 16-row MMA tile),
+// 16-bit operands, 8 * MH query rows per CTA (one or both halves of a 16-row MMA tile),
 // keys split over a cluster.  Bound
 // by the cache bandwidth, so the tensor work runs on warp-level MMAs (m16n8k16)
 // whose operands and results stay in registers: a 128-row tcgen05 tile would do
-// the element work of 128 rows for the 1..32 that exist.  Warp w of 4 owns keys
+// the element work of 128 rows for the 1..16 that exist.  Warp w of 4 owns keys
 // 16 w .. 16 w + 15 of every 64-key tile for all the rows: S = Q K^T, the element
 // work and O += P V need no exchange between warps until the end.  A fifth warp
 // streams K, V (TMA, one box per page part, 128B swizzle), key times and the
@@ -322,17 +320,18 @@ struct PgsSmem {
   static constexpr uint32_t kK = 0;
   static constexpr uint32_t kV = kK + PGS_STAGES * PGS_TILE_BYTES;
   static constexpr uint32_t kSide = kV + PGS_STAGES * PGS_TILE_BYTES;  // per stage: times, biases
-  static constexpr uint32_t kSideBytes = PGS_KEYS * 8 + (PGS_KEYS + 32 + 8) * 4;
+  static constexpr uint32_t kSideBytes = PGS_KEYS * 8 + (PGS_KEYS + 16 + 4) * 4;
   static constexpr uint32_t kTime = kSide + PGS_STAGES * kSideBytes;
   static constexpr uint32_t kThr = kTime + MAX_TIME_BUCKETS * 4;
   static constexpr uint32_t kOct = kThr + MAX_TIME_BUCKETS * 4;
   static constexpr uint32_t kOrt = kOct + 32 * 16;
-  static constexpr uint32_t kMl = kOrt + 32 * 16;                  // warps x 32 rows float2
-  static constexpr uint32_t kMlC = kMl + PGS_WARPS * 32 * 8;       // 32 rows float2 of the CTA
-  static constexpr uint32_t kBars = kMlC + 32 * 8;
+  static constexpr uint32_t kMl = kOrt + 32 * 16;                  // warps x 16 rows float2
+  static constexpr uint32_t kMlC = kMl + PGS_WARPS * 16 * 8;       // 16 rows float2 of the CTA
+  static constexpr uint32_t kBars = kMlC + 16 * 8;
   static constexpr uint32_t kAbort = kBars + 2 * PGS_STAGES * 8;
   static constexpr uint32_t kBytes = kAbort + 16 + 1024;           // + align slack
-  static_assert(PGS_WARPS * 32 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
+  static_assert(kSide % 16 == 0 && kSideBytes % 16 == 0, "bulk copies");
+  static_assert(PGS_WARPS * 16 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
 };
 
 // Copy of `bytes` contiguous bytes (16-byte aligned, a multiple of 16) completing on an mbarrier.
@@ -445,10 +444,9 @@ __device__ __forceinline__ void paged_store(const PagedParams& p, int64_t row, i
 }
 
 template <int PHI, bool F16, int MH>
-__global__ void __launch_bounds__(PGS_THREADS, MH <= 2 ? 3 : 2)
+__global__ void __launch_bounds__(PGS_THREADS, 3)
 hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ PagedParams p) {
-  constexpr int MT = (MH + 1) / 2;  // 16-row MMA tiles
-  constexpr int R = 16 * MT;
+  constexpr int R = 8 * MH;
   constexpr bool kSoftmax = PHI == HSTU_ACT_SOFTMAX;
   constexpr float kScale = phi_scale<PHI>();
   constexpr int kBand = PGS_KEYS + R + 4;  // biases of a tile, from a multiple of 4 down
@@ -599,14 +597,12 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   }
 
   // ---------------- compute warps
-  float o[MT][8][4];
+  float o[8][4];
   float m_run[MH], l_run[MH];
 #pragma unroll
-  for (int a = 0; a < MT; ++a)
+  for (int b = 0; b < 8; ++b)
 #pragma unroll
-    for (int b = 0; b < 8; ++b)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[a][b][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) o[b][e] = 0.0f;
 #pragma unroll
   for (int a = 0; a < MH; ++a) {
     m_run[a] = -INFINITY;
@@ -627,12 +623,12 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       sOrt[tid] = make_float4(tb(o4.w), tb(o4.w + 1), tb(o4.w + 2), tb(o4.w + 3));
     }
     named_barrier_sync(1, PGS_WARPS * 32);
-    uint32_t qf[MT][4][4];
+    uint32_t qf[4][4];
     int32_t ti[MH];
     int64_t bound[MH];  // latest time still in the row's current bucket
-    float rt[MH];
+    float rt[MH];       // and its bias
 #pragma unroll
-    for (int a = 0; a < 2 * MT; ++a) {  // rows gr + 8 a
+    for (int a = 0; a < 2; ++a) {  // rows gr + 8 a
       const int r = gr + 8 * a;
       const bool in = r < rows;
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + (s.q0 + r0 + (in ? r : 0)) * p.ldq + h * 64;
@@ -640,8 +636,7 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          qf[a >> 1][k][(a & 1) + 2 * e] =
-              in ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * e + 2 * tq)) : 0u;
+          qf[k][a + 2 * e] = in ? __ldg(reinterpret_cast<const uint32_t*>(q + 16 * k + 8 * e + 2 * tq)) : 0u;
       if (a < MH) {
         ti[a] = in ? paged_rel(p.q_ts[s.q0 + r0 + r], t_last) : PG_T0;
         bound[a] = INT64_MIN;  // the first chunk looks its buckets up
@@ -658,148 +653,101 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
     // the tiles [f_lo, f_hi) of the list that every row sees whole
     const int f_lo = p.window == 0 ? 0 : s.n_sink + max(0, (i_last - p.window + PGS_KEYS) / PGS_KEYS - s.first);
     const int f_hi = s.n_sink + (i0 + 1) / PGS_KEYS - s.first;
-    int it = 0;
-    // N tiles, the k-th of the list on being the CTA's it-th on; false after a failed wait
-    auto step = [&](auto n_c, int kk) -> bool {
-      constexpr int N = decltype(n_c)::value;
-      int j0[N];
-      uint32_t soff[N];
-      const int64_t* side_t[N];
-      float sc[N][MT][2][4];
-      uint32_t pf[N][MT][4];
-      bool ragged[N], steady[N], full[N], ok = true;
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        const int st = (it + t) % PGS_STAGES;
-        ok = ok && mbar_wait(&bar_full[st], ((it + t) / PGS_STAGES) & 1, ctl);
-        j0[t] = s.tile(kk + t) * PGS_KEYS + wk;  // this warp's first key
-        soff[t] = st * PGS_TILE_BYTES;
-        side_t[t] = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
-        // every row sees every key of this warp; some key is seen by no row
-        full[t] = true;
-        ragged[t] = false;
-        if (kk + t < f_lo || kk + t >= f_hi) {
-          full[t] = j0[t] + 15 <= i0 && (p.window == 0 || j0[t] > i_last - p.window || j0[t] + 16 <= p.sinks);
-          ragged[t] = j0[t] + 16 > s.n || (j0[t] < s.lo && j0[t] + 16 > s.sink_end);
-        }
+    int st = 0;
+    uint32_t ph = 0;
+    for (int kk = k_begin; kk < k_end; ++kk) {
+      const bool ok = mbar_wait(&bar_full[st], ph, ctl);
+      const int j_tile = s.tile(kk) * PGS_KEYS, j0 = j_tile + wk;  // this warp's first key
+      const uint32_t soff = st * PGS_TILE_BYTES;
+      const int64_t* times = reinterpret_cast<const int64_t*>(smem + PgsSmem::kSide + st * PgsSmem::kSideBytes);
+      // every row sees every key of this warp; some key is seen by no row
+      bool full = true, ragged = false;
+      if (kk < f_lo || kk >= f_hi) {
+        full = j0 + 15 <= i0 && (p.window == 0 || j0 > i_last - p.window || j0 + 16 <= p.sinks);
+        ragged = j0 + 16 > s.n || (j0 < s.lo && j0 + 16 > s.sink_end);
       }
-      if (!__all_sync(0xffffffffu, ok)) return false;
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
-        // times a NaN is a NaN, so they are cleared
-        if (ragged[t]) {
-          for (int e = lane; e < 16 * 8; e += 32)
-            if (!s.seen(j0[t] + (e >> 3)))
-              *reinterpret_cast<uint4*>(smem + PgsSmem::kV + soff[t] + (wk + (e >> 3)) * 128 + (e & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+      if (!__all_sync(0xffffffffu, ok)) break;
+      // rows of V that no row sees may hold anything (a page's unwritten slots): P = 0
+      // times a NaN is a NaN, so they are cleared
+      if (ragged) {
+        for (int e = lane; e < 16 * 8; e += 32)
+          if (!s.seen(j0 + (e >> 3)))
+            *reinterpret_cast<uint4*>(smem + PgsSmem::kV + soff + (wk + (e >> 3)) * 128 + (e & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
       }
+      float sc[2][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int t = 0; t < N; ++t) {
-          uint32_t kf[4];
-          ldsm_x4(kaddr + soff[t] + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
-#pragma unroll
-          for (int a = 0; a < MT; ++a) {
-            if (MT > 1 && 16 * a >= rows) continue;
-            if (k == 0) {
-              mma_m16n8k16_first<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
-              mma_m16n8k16_first<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
-            } else {
-              mma_m16n8k16<F16>(sc[t][a][0], qf[a][k], kf[0], kf[1]);
-              mma_m16n8k16<F16>(sc[t][a][1], qf[a][k], kf[2], kf[3]);
-            }
-          }
-        }
-      // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        // row 0, column 0 of this warp
-        const int j_tile = j0[t] - wk;
-        const float* band = reinterpret_cast<const float*>(side_t[t] + PGS_KEYS) + (i0 - j0[t]) -
-                            paged_band0(i0 - j_tile, PGS_KEYS);
-        // Time bucket of a row: it only falls along the keys, so while the chunk's last key
-        // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
-        // no row sees have no time: such chunks look every bucket up, and leave no bound.
-        const int64_t t_end = side_t[t][wk + 15];
-        steady[t] = !ragged[t];
-#pragma unroll
-        for (int a = 0; a < MH; ++a) steady[t] = steady[t] && t_end <= bound[a];
-        steady[t] = __all_sync(0xffffffffu, steady[t]);
-        float rtv[MH][4];
-        if (steady[t]) {
-#pragma unroll
-          for (int a = 0; a < MH; ++a)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) rtv[a][e] = rt[a];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t kf[4];
+        ldsm_x4(kaddr + soff + (((2 * k + kch) ^ (krow & 7)) << 4), kf);
+        if (k == 0) {
+          mma_m16n8k16_first<F16>(sc[0], qf[k], kf[0], kf[1]);
+          mma_m16n8k16_first<F16>(sc[1], qf[k], kf[2], kf[3]);
         } else {
-          // the earliest visible event is among the CTA's first keys
-          if (it == 0 && t == 0 && lane < 16 && s.seen(j0[t] + lane) && t_last - side_t[t][wk + lane] > PG_T0)
-            record_status(HSTU_ERR_DEVICE_CHECK);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int32_t kt = paged_rel(side_t[t][wk + 8 * (e >> 1) + 2 * tq + (e & 1)], t_last);
-#pragma unroll
-            for (int a = 0; a < MH; ++a) rtv[a][e] = time_bias_octave(ti[a] - kt, sOct, sOrt);
-          }
-#pragma unroll
-          for (int a = 0; a < MH; ++a) {
-            // the bucket of the chunk's last key holds until a key passes its edge
-            const int bk = time_bucket_octave(ti[a] - paged_rel(t_end, t_last), sOct);
-            rt[a] = sTime[bk];
-            bound[a] = ragged[t] ? INT64_MIN : (bk == 0 ? INT64_MAX : t_last - PG_T0 + (ti[a] - sThr[bk]));
-          }
-        }
-#pragma unroll
-        for (int a = 0; a < MH; ++a) {
-          if (MH == 4 && 8 * a >= rows) {  // rows of this half do not exist
-            pf[t][a >> 1][(a & 1)] = pf[t][a >> 1][(a & 1) + 2] = 0u;
-            continue;
-          }
-          const int r = gr + 8 * a;
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            x[e] = fmaf(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] + band[r - (8 * (e >> 1) + 2 * tq + (e & 1))],
-                        kScale, rtv[a][e]);
-          const int i = i0 + r;
-          auto vis = [&](int e) {
-            const int j = j0[t] + 8 * (e >> 1) + 2 * tq + (e & 1);
-            return j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
-          };
-          if constexpr (kSoftmax) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] = full[t] || vis(e) ? x[e] : -INFINITY;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if constexpr (PHI == HSTU_ACT_SILU) x[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
-              else if constexpr (PHI == HSTU_ACT_RELU) x[e] = fmaxf(x[e], 0.0f);
-              if (!full[t]) x[e] = vis(e) ? x[e] : 0.0f;
-            }
-            // P in the operand type: the MMA takes both operands in one type
-            pf[t][a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
-            pf[t][a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
-          }
+          mma_m16n8k16<F16>(sc[0], qf[k], kf[0], kf[1]);
+          mma_m16n8k16<F16>(sc[1], qf[k], kf[2], kf[3]);
         }
       }
-      if constexpr (kSoftmax) {
-        // P = 2^(x - m) with a running m that follows the rows' maxima only when one of them
-        // is more than 8 above it: P stays below 2^8, no sum loses anything, and most
-        // steps need neither the quad's maximum nor a rescaled O
+      // ---- element work: columns wk + 8 b + 2 tq + {0, 1}, rows gr + 8 a
+      // bias of row 0, this warp's column 0
+      const float* band =
+          reinterpret_cast<const float*>(times + PGS_KEYS) + (i0 - j0) - paged_band0(i0 - j_tile, PGS_KEYS);
+      // Time bucket of a row: it only falls along the keys, so while the chunk's last key
+      // has not passed the row's edge (`bound`) the row's one bias holds.  Keys that
+      // no row sees have no time: such chunks look every bucket up, and leave no bound.
+      const int64_t t_end = times[wk + 15];
+      bool steady = !ragged;
+#pragma unroll
+      for (int a = 0; a < MH; ++a) steady = steady && t_end <= bound[a];
+      steady = __all_sync(0xffffffffu, steady);
+      float rtv[MH][4];
+      if (steady) {
+#pragma unroll
+        for (int a = 0; a < MH; ++a)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rtv[a][e] = rt[a];
+      } else {
+        // the earliest visible event is among the CTA's first keys
+        if (kk == k_begin && lane < 16 && s.seen(j0 + lane) && t_last - times[wk + lane] > PG_T0)
+          record_status(HSTU_ERR_DEVICE_CHECK);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int32_t kt = paged_rel(times[wk + 8 * (e >> 1) + 2 * tq + (e & 1)], t_last);
+#pragma unroll
+          for (int a = 0; a < MH; ++a) rtv[a][e] = time_bias_octave(ti[a] - kt, sOct, sOrt);
+        }
 #pragma unroll
         for (int a = 0; a < MH; ++a) {
-          if (MH == 4 && 8 * a >= rows) continue;
+          // the bucket of the chunk's last key holds until a key passes its edge
+          const int bk = time_bucket_octave(ti[a] - paged_rel(t_end, t_last), sOct);
+          rt[a] = sTime[bk];
+          bound[a] = ragged ? INT64_MIN : (bk == 0 ? INT64_MAX : t_last - PG_T0 + (ti[a] - sThr[bk]));
+        }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int a = 0; a < MH; ++a) {
+        const int r = gr + 8 * a, i = i0 + r;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = fmaf(sc[e >> 1][2 * a + (e & 1)] + band[r - (8 * (e >> 1) + 2 * tq + (e & 1))], kScale, rtv[a][e]);
+        auto vis = [&](int e) {
+          const int j = j0 + 8 * (e >> 1) + 2 * tq + (e & 1);
+          return j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
+        };
+        if constexpr (kSoftmax) {
+          // P = 2^(x - m) with a running m that follows the rows' maxima only when one of them
+          // is more than 8 above it: P stays below 2^8, no sum loses anything, and most
+          // tiles need neither the quad's maximum nor a rescaled O
           float cm = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < N; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cm = fmaxf(cm, sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)]);
+          for (int e = 0; e < 4; ++e) {
+            if (!full) x[e] = vis(e) ? x[e] : -INFINITY;
+            cm = fmaxf(cm, x[e]);
+          }
           if (__any_sync(0xffffffffu, cm > m_run[a] + 8.0f)) {
             cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 1));
             cm = fmaxf(cm, __shfl_xor_sync(0xffffffffu, cm, 2));
@@ -809,67 +757,60 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
             l_run[a] *= f;
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
-              o[a >> 1][b][2 * (a & 1)] *= f;
-              o[a >> 1][b][2 * (a & 1) + 1] *= f;
+              o[b][2 * a] *= f;
+              o[b][2 * a + 1] *= f;
             }
           }
           const float mm = m_run[a] > -INFINITY ? m_run[a] : 0.0f;
 #pragma unroll
-          for (int t = 0; t < N; ++t) {
-            float x[4];
+          for (int e = 0; e < 4; ++e) {
+            x[e] = ex2_approx(x[e] - mm);
+            l_run[a] += x[e];
+          }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[e] = ex2_approx(sc[t][a >> 1][e >> 1][2 * (a & 1) + (e & 1)] - mm);
-              l_run[a] += x[e];
-            }
-            pf[t][a >> 1][(a & 1)] = pack_16<F16>(x[0], x[1]);
-            pf[t][a >> 1][(a & 1) + 2] = pack_16<F16>(x[2], x[3]);
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (PHI == HSTU_ACT_SILU) x[e] = fmaf(x[e], tanh_approx(x[e]), x[e]);
+            else if constexpr (PHI == HSTU_ACT_RELU) x[e] = fmaxf(x[e], 0.0f);
+            if (!full) x[e] = vis(e) ? x[e] : 0.0f;
           }
         }
+        // P in the operand type: the MMA takes both operands in one type
+        pf[a] = pack_16<F16>(x[0], x[1]);
+        pf[a + 2] = pack_16<F16>(x[2], x[3]);
       }
-      if constexpr (MH == 1)  // rows 8 .. 15 do not exist
-#pragma unroll
-        for (int t = 0; t < N; ++t) pf[t][0][1] = pf[t][0][3] = 0u;
+      if constexpr (MH == 1) pf[1] = pf[3] = 0u;  // rows 8 .. 15 do not exist
       // ---- O += P V
 #pragma unroll
-      for (int t = 0; t < N; ++t)
-#pragma unroll
-        for (int b = 0; b < 8; b += 2) {
-          uint32_t vf[4];
-          ldsm_x4_t(vaddr + soff[t] + (((b + vch) ^ (vrow & 7)) << 4), vf);
-#pragma unroll
-          for (int a = 0; a < MT; ++a) {
-            if (MT > 1 && 16 * a >= rows) continue;
-            mma_m16n8k16<F16>(o[a][b], pf[t][a], vf[0], vf[1]);
-            mma_m16n8k16<F16>(o[a][b + 1], pf[t][a], vf[2], vf[3]);
-          }
-        }
+      for (int b = 0; b < 8; b += 2) {
+        uint32_t vf[4];
+        ldsm_x4_t(vaddr + soff + (((b + vch) ^ (vrow & 7)) << 4), vf);
+        mma_m16n8k16<F16>(o[b], pf, vf[0], vf[1]);
+        mma_m16n8k16<F16>(o[b + 1], pf, vf[2], vf[3]);
+      }
       __syncwarp();
-      if (lane == 0)
-#pragma unroll
-        for (int t = 0; t < N; ++t) mbar_arrive(&bar_empty[(it + t) % PGS_STAGES]);
-      it += N;
-      return true;
-    };
-    int kk = k_begin;
-    bool ok = true;
-    for (; ok && kk < k_end; ++kk) ok = step(std::integral_constant<int, 1>{}, kk);
+      if (lane == 0) mbar_arrive(&bar_empty[st]);
+      if (++st == PGS_STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
+    }
   }
   __syncthreads();  // the stages are idle: the partial sums go over them
   float* sO = reinterpret_cast<float*>(smem);
   if (warp < PGS_WARPS) {
 #pragma unroll
-    for (int a = 0; a < 2 * MT; ++a) {
+    for (int a = 0; a < MH; ++a) {
       const int r = gr + 8 * a;
 #pragma unroll
       for (int b = 0; b < 8; ++b)
         *reinterpret_cast<float2*>(sO + (warp * R + r) * PGS_OLD + 8 * b + 2 * tq) =
-            make_float2(o[a >> 1][b][2 * (a & 1)], o[a >> 1][b][2 * (a & 1) + 1]);
-      if (kSoftmax && a < MH) {
-        float l = l_run[a < MH ? a : 0];
+            make_float2(o[b][2 * a], o[b][2 * a + 1]);
+      if constexpr (kSoftmax) {
+        float l = l_run[a];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (tq == 0) sMl[warp * 32 + r] = make_float2(m_run[a < MH ? a : 0], l);
+        if (tq == 0) sMl[warp * R + r] = make_float2(m_run[a], l);
       }
     }
   }
@@ -885,10 +826,10 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
       for (int w = 0; w < PGS_WARPS; ++w) f[w] = 1.0f;
       if constexpr (kSoftmax) {
 #pragma unroll
-        for (int w = 0; w < PGS_WARPS; ++w) m = fmaxf(m, sMl[w * 32 + r].x);
+        for (int w = 0; w < PGS_WARPS; ++w) m = fmaxf(m, sMl[w * R + r].x);
 #pragma unroll
         for (int w = 0; w < PGS_WARPS; ++w) {
-          const float2 v = sMl[w * 32 + r];
+          const float2 v = sMl[w * R + r];
           f[w] = v.x > -INFINITY ? ex2_approx(v.x - m) : 0.0f;
           l = fmaf(v.y, f[w], l);
         }
