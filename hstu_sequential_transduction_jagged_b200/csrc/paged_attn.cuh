@@ -130,19 +130,19 @@ __device__ __forceinline__ int32_t paged_rel(int64_t t, int64_t t_last) {
 // ---------------------------------------------------------------- fp32
 
 // fp32 layers are small (tens to hundreds of events, one or two heads): FFMA over
-// 64-key tiles in shared memory, 16 query rows per CTA, thread (key or column
-// tid % 64, rows tid / 64 + 4 k).  Exact exponentials (expf), so the result holds
-// fp32 accuracy.  Softmax keeps a running maximum and sum per row.
+// 64-key tiles in shared memory, 16 query rows per CTA, four rows and one key (or
+// one column of V) per thread, 16-byte shared loads; the next tile's rows are read
+// into registers meanwhile.  Exact exponentials (expf), so the result holds fp32
+// accuracy.  Softmax keeps a running maximum and sum per row.
 constexpr int PG32_KEYS = 64;
 constexpr int PG32_ROWS = 16;
 constexpr int PG32_THREADS = 256;
 
 struct Paged32Smem {
   float q[PG32_ROWS][64];
-  float k[PG32_KEYS][65];
-  float v[PG32_KEYS][64];
-  float s[PG32_ROWS][PG32_KEYS + 1];
-  float o[PG32_ROWS][64];       // this CTA's partial sums
+  float k[PG32_KEYS][68];       // rows 4 banks apart: 16-byte loads of 8 lanes do not collide
+  float v[PG32_KEYS][64];       // after the last tile, rows 0 .. 15: this CTA's partial sums
+  float s[PG32_ROWS][PG32_KEYS];
   float2 ml[PG32_ROWS];         // softmax: (max, sum) of this CTA's keys
   float scale[PG32_ROWS];       // softmax: factor of the running sums
   int32_t kt[PG32_KEYS];
@@ -152,7 +152,7 @@ struct Paged32Smem {
 
 __global__ void __launch_bounds__(PG32_THREADS)
 hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
-  __shared__ Paged32Smem sm;
+  __shared__ __align__(16) Paged32Smem sm;
   namespace cg = cooperative_groups;
   const int split = static_cast<int>(blockIdx.x % p.nsplit);
   const int64_t id = blockIdx.x / p.nsplit;
@@ -173,9 +173,51 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
   const int64_t t_last = p.q_ts[s.q0 + s.c - 1];
   const int32_t* tab = p.table + static_cast<int64_t>(s.seq) * p.max_blocks;
   const int ps = 1 << p.ps_log2;
-  for (int e = tid; e < PG32_ROWS * 64; e += PG32_THREADS) {
-    const int r = e >> 6, c = e & 63;
-    sm.q[r][c] = r < rows ? static_cast<const float*>(p.q)[(s.q0 + r0 + r) * p.ldq + h * 64 + c] : 0.0f;
+  const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
+  const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
+  // A tile's rows, 16 bytes per thread and step (step e: K for e < 4, V after; row
+  // tid / 16 + 16 (e % 4)), and a time per thread of the first 64; keys that no row
+  // sees are zeros
+  float4 x[8];
+  int32_t t_new = 0;
+  auto load_tile = [&](int kk) {
+    const int j0 = s.tile(kk) * PG32_KEYS;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + (tid >> 4) + 16 * e;
+      x[e] = x[e + 4] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s.seen(j)) {
+        const int page = tab[j >> p.ps_log2];
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
+          const float4* row = reinterpret_cast<const float4*>(p.kv) +
+                              ((static_cast<int64_t>(page) * 2 * p.H + h) * ps + (j & (ps - 1))) * 16 + (tid & 15);
+          x[e] = __ldg(row);
+          x[e + 4] = __ldg(row + static_cast<int64_t>(p.H) * ps * 16);
+        } else if ((tid & 15) == 0) {
+          record_status(HSTU_ERR_DEVICE_CHECK);
+        }
+      }
+    }
+    if (tid < PG32_KEYS) {
+      const int j = j0 + tid;
+      t_new = 0;
+      if (s.seen(j)) {
+        const int page = tab[j >> p.ps_log2];
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
+          const int64_t tj = p.ts[static_cast<int64_t>(page) * ps + (j & (ps - 1))];
+          if (t_last - tj > PG_T0) record_status(HSTU_ERR_DEVICE_CHECK);
+          t_new = paged_rel(tj, t_last);
+        }
+      }
+    }
+  };
+  if (k_begin < k_end) load_tile(k_begin);
+  {
+    const int r = tid >> 4, c4 = tid & 15;
+    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r < rows)
+      q = *(reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + (s.q0 + r0 + r) * p.ldq + h * 64) + c4);
+    *reinterpret_cast<float4*>(&sm.q[r][4 * c4]) = q;
   }
   for (int e = tid; e < p.Tb; e += PG32_THREADS) sm.rt[e] = p.rab_time[static_cast<int64_t>(h) * p.Tb + e];
   if (tid < PG32_ROWS) {
@@ -184,78 +226,61 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
   }
   const int col = tid & 63, rg = tid >> 6;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int k_begin = static_cast<int>(static_cast<int64_t>(s.n_tiles) * split / p.nsplit);
-  const int k_end = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (split + 1) / p.nsplit);
   const float* rp = p.rab_pos + static_cast<int64_t>(h) * p.P;
   for (int kk = k_begin; kk < k_end; ++kk) {
     const int j0 = s.tile(kk) * PG32_KEYS;
     __syncthreads();
-    // the tile's rows, 16 bytes per thread and step; keys that no row sees are zeros
-    for (int e = tid; e < 2 * PG32_KEYS * 16; e += PG32_THREADS) {
-      const int kv = e >> 10, r = (e >> 4) & 63, c4 = e & 15;
-      const int j = j0 + r;
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (s.seen(j)) {
-        const int page = tab[j >> p.ps_log2];
-        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages))
-          x = reinterpret_cast<const float4*>(p.kv)[
-              (((static_cast<int64_t>(page) * 2 + kv) * p.H + h) * ps + (j & (ps - 1))) * 16 + c4];
-        else if (c4 == 0)
-          record_status(HSTU_ERR_DEVICE_CHECK);
-      }
-      if (kv == 0) {
-        sm.k[r][4 * c4] = x.x;
-        sm.k[r][4 * c4 + 1] = x.y;
-        sm.k[r][4 * c4 + 2] = x.z;
-        sm.k[r][4 * c4 + 3] = x.w;
-      } else {
-        *reinterpret_cast<float4*>(&sm.v[r][4 * c4]) = x;
-      }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = (tid >> 4) + 16 * e;
+      *reinterpret_cast<float4*>(&sm.k[r][4 * (tid & 15)]) = x[e];
+      *reinterpret_cast<float4*>(&sm.v[r][4 * (tid & 15)]) = x[e + 4];
     }
-    if (tid < PG32_KEYS) {
-      const int j = j0 + tid;
-      int32_t t = 0;
-      if (s.seen(j)) {
-        const int page = tab[j >> p.ps_log2];
-        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
-          const int64_t tj = p.ts[static_cast<int64_t>(page) * ps + (j & (ps - 1))];
-          if (tj - t_last + PG_T0 < 0) record_status(HSTU_ERR_DEVICE_CHECK);
-          t = paged_rel(tj, t_last);
-        }
-      }
-      sm.kt[tid] = t;
-    }
+    if (tid < PG32_KEYS) sm.kt[tid] = t_new;
     __syncthreads();
+    if (kk + 1 < k_end) load_tile(kk + 1);
     const int j = j0 + col;
+    float dot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+      const float4 kx = *reinterpret_cast<const float4*>(&sm.k[col][c]);
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const float4 qx = *reinterpret_cast<const float4*>(&sm.q[rg + 4 * a][c]);
+        dot[a] = fmaf(qx.x, kx.x, fmaf(qx.y, kx.y, fmaf(qx.z, kx.z, fmaf(qx.w, kx.w, dot[a]))));
+      }
+    }
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const int r = rg + 4 * a;
-      float dot = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 64; ++c) dot = fmaf(sm.q[r][c], sm.k[col][c], dot);
-      const int i = i0 + r;
+      const int r = rg + 4 * a, i = i0 + r;
       const bool vis = r < rows && j <= i && (p.window == 0 || j > i - p.window || j < p.sinks);
-      float x = dot;
-      if (vis) {
-        const int b = time_bucket_octave(sm.qt[r] - sm.kt[col], p.oct);
-        x += rp[min(i - j, p.P - 1)] + sm.rt[b];
-      }
-      sm.s[r][col] = softmax ? (vis ? x : -INFINITY) : (vis ? phi_runtime(x, phi2) : 0.0f);
+      float y = dot[a];
+      if (vis) y += __ldg(rp + min(i - j, p.P - 1)) + sm.rt[time_bucket_octave(sm.qt[r] - sm.kt[col], p.oct)];
+      sm.s[r][col] = softmax ? (vis ? y : -INFINITY) : (vis ? phi_runtime(y, phi2) : 0.0f);
     }
     __syncthreads();
     if (softmax) {
-      if (tid < PG32_ROWS) {
-        float m = sm.ml[tid].x;
-        for (int c = 0; c < PG32_KEYS; ++c) m = fmaxf(m, sm.s[tid][c]);
-        const float f = m > -INFINITY ? expf(sm.ml[tid].x - m) : 1.0f;
-        float l = sm.ml[tid].y * f;
-        for (int c = 0; c < PG32_KEYS; ++c) {
-          const float e = m > -INFINITY ? expf(sm.s[tid][c] - m) : 0.0f;
-          sm.s[tid][c] = e;
-          l += e;
-        }
-        sm.scale[tid] = f;
-        sm.ml[tid] = make_float2(m, l);
+      // 16 lanes a row, four keys each
+      const int r = tid >> 4, c4 = tid & 15;
+      float4 y = *reinterpret_cast<const float4*>(&sm.s[r][4 * c4]);
+      float m = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float2 old = sm.ml[r];
+      m = fmaxf(m, old.x);
+      const bool any = m > -INFINITY;
+      y.x = any ? expf(y.x - m) : 0.0f;
+      y.y = any ? expf(y.y - m) : 0.0f;
+      y.z = any ? expf(y.z - m) : 0.0f;
+      y.w = any ? expf(y.w - m) : 0.0f;
+      *reinterpret_cast<float4*>(&sm.s[r][4 * c4]) = y;
+      float l = (y.x + y.y) + (y.z + y.w);
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (c4 == 0) {
+        const float f = any ? expf(old.x - m) : 1.0f;
+        sm.scale[r] = f;
+        sm.ml[r] = make_float2(m, fmaf(old.y, f, l));
       }
       __syncthreads();
 #pragma unroll
@@ -263,19 +288,24 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
     }
     // each tile's sum apart, then added: the rounding grows with the tiles, not the keys
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < PG32_KEYS; ++c) {
-      const float vv = sm.v[c][col];
+#pragma unroll 4
+    for (int c = 0; c < PG32_KEYS; c += 4) {
+      const float v0 = sm.v[c][col], v1 = sm.v[c + 1][col], v2 = sm.v[c + 2][col], v3 = sm.v[c + 3][col];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) part[a] = fmaf(sm.s[rg + 4 * a][c], vv, part[a]);
+      for (int a = 0; a < 4; ++a) {
+        const float4 w = *reinterpret_cast<const float4*>(&sm.s[rg + 4 * a][c]);
+        part[a] = fmaf(w.x, v0, fmaf(w.y, v1, fmaf(w.z, v2, fmaf(w.w, v3, part[a]))));
+      }
     }
 #pragma unroll
     for (int a = 0; a < 4; ++a) acc[a] += part[a];
   }
+  __syncthreads();
 #pragma unroll
-  for (int a = 0; a < 4; ++a) sm.o[rg + 4 * a][col] = acc[a];
+  for (int a = 0; a < 4; ++a) sm.v[rg + 4 * a][col] = acc[a];
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  // rank `split` writes rows split, split + nsplit, ...: 64 threads per row
+  // rank `split` writes rows 4 split .., 4 (split + nsplit) ..: 64 threads per row
   for (int r = split * 4 + rg; r < rows; r += 4 * p.nsplit) {
     float o = 0.0f;
     if (softmax) {
@@ -285,11 +315,11 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
         const Paged32Smem* o_sm = cluster.map_shared_rank(&sm, k);
         const float f = o_sm->ml[r].x > -INFINITY ? expf(o_sm->ml[r].x - m) : 0.0f;
         l += o_sm->ml[r].y * f;
-        o += o_sm->o[r][col] * f;
+        o += o_sm->v[r][col] * f;
       }
       o = l > 0.0f ? o / l : 0.0f;
     } else {
-      for (int k = 0; k < p.nsplit; ++k) o += cluster.map_shared_rank(&sm, k)->o[r][col];
+      for (int k = 0; k < p.nsplit; ++k) o += cluster.map_shared_rank(&sm, k)->v[r][col];
       o /= static_cast<float>(n_all);
     }
     p.av_f32[((s.q0 + r0 + r) * p.H + h) * 64 + col] = o;
