@@ -180,30 +180,51 @@ hstu_cache_reserve_kernel(const CacheView c, int B, const int32_t* __restrict__ 
     ws.state[0] = bad ? 0 : 1;
     if (bad) record_status(HSTU_ERR_DEVICE_CHECK);
   }
-  // hand out: a warp per user
+  // hand out: a thread per user for its first pages, the warp for the rest of a long one
+  constexpr int OWN = 4;
   const int lane = lane_id();
-  for (int u = warp_id(); u < B; u += CACHE_META_THREADS / 32) {
-    const int seq = seq_ids != nullptr ? seq_ids[u] : u;
+  for (int u0 = 0; u0 < B; u0 += CACHE_META_THREADS) {
+    const int u = u0 + tid;
+    const bool in = u < B;
+    const int seq = !in ? 0 : (seq_ids != nullptr ? seq_ids[u] : u);
     if (bad) {
-      if (lane == 0 && static_cast<uint32_t>(seq) < static_cast<uint32_t>(c.num_seqs))
+      if (in && static_cast<uint32_t>(seq) < static_cast<uint32_t>(c.num_seqs))
         atomicAnd(&c.lengths[seq], INT32_MAX);
       continue;
     }
-    const int n = ws.old_len[u], cnt = static_cast<int>(offsets[u + 1] - offsets[u]);
-    const int have = c.blocks(n), want = c.blocks(n + cnt);
-    const int src = ws.cow[2 * u];
-    const int32_t* mine = ws.pages + ws.first[u];
-    const int off = src >= 0 ? 1 : 0;
-    int32_t* row = c.row(seq);
-    for (int b = have - off + lane; b < want; b += 32) {
-      const int page = mine[b - have + off];
-      row[b] = page;
-      c.ref[page] = 1;
+    int n = 0, cnt = 0, src = -1, first = 0;
+    if (in) {
+      n = ws.old_len[u];
+      cnt = static_cast<int>(offsets[u + 1] - offsets[u]);
+      src = ws.cow[2 * u];
+      first = ws.first[u];
     }
-    if (lane == 0) {
-      ws.cow[2 * u + 1] = src >= 0 ? mine[0] : -1;
+    const int b0 = c.blocks(n) - (src >= 0 ? 1 : 0);  // first block that gets a page
+    const int need = in ? c.blocks(n + cnt) - b0 : 0;
+    int copy = -1;
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+      if (k < need) {
+        const int page = ws.pages[first + k];
+        if (k == 0 && src >= 0) copy = page;
+        c.row(seq)[b0 + k] = page;
+        c.ref[page] = 1;
+      }
+    }
+    if (in) {
+      ws.cow[2 * u + 1] = copy;
       if (src >= 0) atomicSub(&c.ref[src], 1);
       c.lengths[seq] = n + cnt;
+    }
+    for (unsigned m = __ballot_sync(0xffffffffu, need > OWN); m != 0u; m &= m - 1u) {
+      const int w = __ffs(m) - 1;
+      const int need_w = __shfl_sync(0xffffffffu, need, w), first_w = __shfl_sync(0xffffffffu, first, w);
+      int32_t* row = c.row(__shfl_sync(0xffffffffu, seq, w)) + __shfl_sync(0xffffffffu, b0, w);
+      for (int k = OWN + lane; k < need_w; k += 32) {
+        const int page = ws.pages[first_w + k];
+        row[k] = page;
+        c.ref[page] = 1;
+      }
     }
   }
 }
