@@ -119,7 +119,7 @@ const int4* octaves_for(int Tb) {
 enum KernelKind : int {
   K_F1 = 0, K_ATTN, K_F2, K_CAND_ATTN, K_SCORE, K_F32_LINEAR, K_F32_ATTN, K_F32_LN, K_CVT,
   K_SL, K_SL_GATHER, K_ATTN_FUSED, K_ATTN_BWD, K_BWD_GEMM, K_GATE_BWD,
-  K_BWD_ELT, K_CACHE_META, K_CACHE_ROWS, K_PAGED_ATTN, K_COUNT
+  K_BWD_ELT, K_CACHE_META, K_CACHE_ROWS, K_PAGED_ROWS, K_PAGED_TILE, K_PAGED_F32, K_COUNT
 };
 const char* const kKernelNames[K_COUNT] = {"f1_gemm",     "attention",      "f2_gemm",
                                            "mfalcon_attention", "score",    "fp32_linear",
@@ -127,7 +127,8 @@ const char* const kKernelNames[K_COUNT] = {"f1_gemm",     "attention",      "f2_
                                            "sl_select",         "sl_gather",
                                            "attention_f2_fused", "attention_bwd",
                                            "bwd_gemm_cublas", "gate_bwd", "bwd_elementwise",
-                                           "cache_pages", "cache_rows", "paged_attention"};
+                                           "cache_pages", "cache_rows", "paged_attention_rows",
+                                           "paged_attention_tile", "paged_attention_fp32"};
 
 struct Profiler {
   std::mutex mu;
@@ -1024,8 +1025,28 @@ struct PagedJob {
   const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
 };
 
-// Rows per sequence from which the many-rows kernel is taken.
-int paged_tile_min_rows(int phi2) { return phi2 == HSTU_ACT_SOFTMAX ? 64 : 32; }
+// Whether the many-rows kernel is the faster one, by what a CTA of each kernel takes
+// (microseconds on B200): a start and an end of 5 (rows) or 9 (tile), and per key tile
+// 0.5 / 0.75 / 1.0 with 1 / 2 / 3 CTAs on the SM (rows, 16 query rows), or 0.85 up to
+// 128 query rows and 1.25 up to 256 (tile; the softmax's two passes twice that).  A
+// last round of CTAs that is not full counts half.  Measured, 8 heads, 4096 events,
+// rows against tile: 16 users x 32 events 51 and 57, x 64 95 and 57 (softmax 112 and
+// 131), x 128 180 and 58 (softmax 234 and 131); 64 users x 24 events over 1024 65 and
+// 74; 2 users, 2 heads, 47 events over 157 7 and 13.
+bool paged_tile_is_faster(int64_t rows_ctas, int rows_ns, int64_t tile_ctas, int tile_ns, int tiles,
+                          int max_new, bool softmax, int sm_count) {
+  auto rounds = [](int64_t ctas, int64_t slots) {
+    const double r = static_cast<double>(ctas) / static_cast<double>(slots);
+    return r <= 1.0 ? 1.0 : 0.5 * (r + std::ceil(r));
+  };
+  auto share = [&](int ns) { return std::ceil(static_cast<double>(tiles) / ns); };
+  const int64_t rc = rows_ctas * rows_ns;
+  const double resident = std::min<double>(3.0, std::ceil(static_cast<double>(rc) / sm_count));
+  const double rows = 5.0 + rounds(rc, 3ll * sm_count) * share(rows_ns) * (0.25 + 0.25 * resident);
+  const double per_tile = (max_new <= 128 ? 0.85 : 1.25) * (softmax ? 2.0 : 1.0);
+  const double tile = 9.0 + rounds(tile_ctas * tile_ns, sm_count) * share(tile_ns) * per_tile;
+  return tile < rows;
+}
 
 // CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
 // while the grid stays within 1.1 times what the SMs hold at once (`slots`) and the
@@ -1118,11 +1139,11 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   auto busy = [&](int rows) {
     return std::min<int64_t>(static_cast<int64_t>(p.B) * p.groups, p.T / rows + p.B) * p.H;
   };
-  ProfScope prof(K_PAGED_ATTN, st);
   if (ca->dtype == HSTU_FP32) {
     p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
     p.nsplit = paged_splits(busy(PG32_ROWS), 4 * di->sm_count, tiles_of(PG32_KEYS));
+    ProfScope prof(K_PAGED_F32, st);
     return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
   }
   const bool f16 = ca->dtype == HSTU_FP16;
@@ -1130,21 +1151,31 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
   if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, 64), f16)) != HSTU_OK)
     return s;
-  if (max_new > paged_tile_min_rows(c->phi2)) {
+  static_assert(PGS_KEYS == PGT_KEYS, "one count of key tiles for both kernels");
+  const int tiles = tiles_of(PGS_KEYS);
+  const int tile_groups = (max_new + PGT_ROWS - 1) / PGT_ROWS;
+  p.groups = tile_groups;
+  const int64_t tile_busy = busy(PGT_ROWS);
+  const int tile_ns = paged_splits(tile_busy, di->sm_count, tiles);
+  const int mh = max_new <= 8 ? 1 : 2;  // 8-row halves per CTA of the few-rows kernel
+  p.groups = (max_new + 8 * mh - 1) / (8 * mh);
+  const int64_t rows_busy = busy(8 * mh);
+  p.nsplit = paged_splits(rows_busy, 3 * di->sm_count, tiles);
+  if (max_new > 16 && paged_tile_is_faster(rows_busy, p.nsplit, tile_busy, tile_ns, tiles, max_new,
+                                           c->phi2 == HSTU_ACT_SOFTMAX, di->sm_count)) {
     CUtensorMap mq;
     const int64_t hc = static_cast<int64_t>(p.H) * 64;
     if ((s = make_map_16(&mq, q, p.T, hc, ldq, 64, 128, f16)) != HSTU_OK) return s;
-    p.groups = (max_new + PGT_ROWS - 1) / PGT_ROWS;
+    p.groups = tile_groups;
+    p.nsplit = tile_ns;
     const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(busy(PGT_ROWS), di->sm_count, tiles_of(PGT_KEYS));
+    ProfScope prof(K_PAGED_TILE, st);
     return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), ctas, p.nsplit, PGT_THREADS, PgtSmem::kBytes, st,
                           mq, mkv, p);
   }
-  const int mh = max_new <= 8 ? 1 : 2;
-  p.groups = (max_new + 8 * mh - 1) / (8 * mh);
   const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.nsplit = paged_splits(busy(8 * mh), 3 * di->sm_count, tiles_of(PGS_KEYS));
   p.sorted = p.B > 1 && p.B <= 128 && ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
+  ProfScope prof(K_PAGED_ROWS, st);
   return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);
 }

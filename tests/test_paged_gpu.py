@@ -92,7 +92,7 @@ LENS = [(1, 1), (5, 5), (64, 1), (65, 1), (130, 2), (300, 17), (0, 0), (257, 40)
 
 
 def run_attn(H, lens, heads, dtype, phi2, ps, window=0, sinks=0, Pb=64, Tb=64, gap="exp", seed=7, f32=False,
-             release=False, spread=None):
+             release=False, kernel=None):
     counts = [c for _, c in lens]
     ac = make_attn_case([n for n, _ in lens], heads, Pb, Tb, seed=seed, dtype=dtype, gap_kind=gap)
     total = sum(-(-n // ps) for n, _ in lens)
@@ -110,7 +110,10 @@ def run_attn(H, lens, heads, dtype, phi2, ps, window=0, sinks=0, Pb=64, Tb=64, g
     rp, rt = tensor(ac.rab_pos, torch.float32, "cuda"), tensor(ac.rab_time, torch.float32, "cuda")
     wide = torch.cat([torch.full_like(q, float("nan")), q], 1)  # a row stride, NaN beside the rows
     args = (cfg, cache, 1, j, wide[:, heads * 64:], rp, rt, max(n for n, _ in lens))
+    H.profiler_start()
     got = fn(*args, window=window, sinks=sinks, seq_ids=seq)
+    ran = set(H.profiler_stop())
+    assert kernel is None or ran == {"paged_attention_" + kernel}, ran
     again = fn(*args, window=window, sinks=sinks, seq_ids=seq)
     assert H.device_status() == 0
     assert torch.equal(got, again)  # the same bits
@@ -180,14 +183,38 @@ def test_attention_one_row_of_many_lengths(H):
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("phi2", ["silu", "softmax"])
 def test_attention_long_chunks(H, dtype, phi2):
-    run_attn(H, [(700, 700), (1300, 300), (400, 1), (600, 257), (520, 65)], 2, dtype, phi2, 64, Pb=600)
+    run_attn(H, [(700, 700), (1300, 300), (400, 1), (600, 257), (520, 65)], 6, dtype, phi2, 64, Pb=600, kernel="tile")
+
+
+@pytest.mark.parametrize("ps", [16, 32, 128])
+@pytest.mark.parametrize("phi2", ["silu", "relu", "identity", "softmax"])
+def test_attention_tiles(H, phi2, ps):
+    """The many-rows kernel: one query tile and two, ragged, short contexts, empty ones."""
+    lens = [(128, 128), (129, 129), (256, 256), (257, 257), (300, 100), (64, 64), (0, 0), (63, 1), (700, 130), (90, 0),
+            (400, 128), (333, 33), (1, 1)] * 2
+    run_attn(H, lens, 8, "fp16", phi2, ps, kernel="rows" if phi2 == "softmax" else "tile")
+    short = [(n, min(n, 120)) for n, _ in lens] * 3
+    run_attn(H, short, 6, "bf16", phi2, ps, Pb=2000, Tb=128, gap="lognormal", kernel="tile")
+
+
+@pytest.mark.parametrize("phi2", ["silu", "softmax"])
+@pytest.mark.parametrize("new", [17, 40, 100])
+def test_attention_rows_in_groups(H, phi2, new):
+    """The few-rows kernel takes chunks of more than its 16 rows in groups."""
+    run_attn(H, [(200, new), (333, new - 1), (130, 1)], 2, "fp16", phi2, 32, kernel="rows")
 
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (50, 10), (300, 129), (128, 64)])
 def test_attention_long_chunks_window(H, dtype, window, sinks):
-    run_attn(H, [(1500, 600), (1300, 300), (400, 1), (257, 257)], 1, dtype, "silu", 32, window=window,
-             sinks=sinks, Pb=2048, gap="lognormal")
+    run_attn(H, [(1500, 600), (1300, 300), (400, 1), (257, 257)], 6, dtype, "silu", 32, window=window,
+             sinks=sinks, Pb=2048, gap="lognormal", kernel="tile")
+
+
+def test_attention_tiles_over_released_pages(H):
+    lens = [(1500, 100), (1300, 120), (400, 1), (700, 64)] * 6
+    cache = run_attn(H, lens, 8, "fp16", "silu", 16, window=200, sinks=50, Pb=2048, release=True, kernel="tile")
+    assert int((cache.block_table[:, :30] < 0).sum()) > 100
 
 
 def test_far_offsets_in_a_large_cache(H):
