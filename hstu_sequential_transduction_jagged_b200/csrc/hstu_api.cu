@@ -1049,14 +1049,18 @@ bool paged_tile_is_faster(int64_t rows_ctas, int rows_ns, int64_t tile_ctas, int
 }
 
 // CTAs per cluster: a power of two (others pack badly) up to 8, the portable size,
-// while the grid stays within 1.1 times what the SMs hold at once (`slots`) and the
-// longest context has that many key tiles.  More CTAs than that only add startups:
-// one event over 4096 for 144 (sequence, head) pairs takes 29 us split in 2, 42 us in 3
-// and 39 us in 4; 16 events for 128 pairs 35 us in 2 and 49 us in 4; one event over
-// 100 .. 4096 for 240 pairs 38 us whole and 32 us in 2 (480 CTAs, 444 slots).
+// while the longest context has that many key tiles and the grid stays within what
+// the SMs hold at once (`slots`), or within 1.1 times that where a CTA keeps 16 key
+// tiles: a second round of CTAs costs a start and an end.  One event over 4096 for 144
+// (sequence, head) pairs takes 29 us split in 2, 42 us in 3 and 39 us in 4; 16 events
+// for 128 pairs 35 us in 2 and 49 us in 4; one event over 100 .. 4096 for 240 pairs
+// 38 us whole and 32 us in 2 (480 CTAs, 444 slots); 9 events over 384 for 120 pairs
+// 19 us in 4 (480 CTAs) and 11 us in 2.
 int paged_splits(int64_t ctas, int64_t slots, int max_tiles) {
   int ns = 1;
-  while (ns < 8 && 10 * ctas * ns * 2 <= 11 * slots && 2 * ns <= max_tiles) ns *= 2;
+  while (ns < 8 && 2 * ns <= max_tiles &&
+         (ctas * ns * 2 <= slots || (10 * ctas * ns * 2 <= 11 * slots && max_tiles >= 32 * ns)))
+    ns *= 2;
   return ns;
 }
 
