@@ -13,7 +13,10 @@
 //
 // The bookkeeping kernels run as one CTA (they are chains of scans over a few
 // thousand integers: latency, not bandwidth) and leave copy lists in the caller's
-// workspace; the copies run as a second launch over all SMs.
+// workspace; the copies run as a second launch over all SMs.  Measured (B200, 4
+// layers, 8 heads): release + fork + reserve of 256 branches of 32 users 35 us, of
+// which 21 us copy 69 MB of partial pages (the copy bandwidth); compact 161 us for
+// 464 MB of pages (5.8 TB/s read and written); append 5.6 and gather 5.8 TB/s.
 #pragma once
 
 #include <cstdint>

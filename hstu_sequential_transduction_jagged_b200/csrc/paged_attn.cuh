@@ -133,7 +133,9 @@ __device__ __forceinline__ int32_t paged_rel(int64_t t, int64_t t_last) {
 // 64-key tiles in shared memory, 16 query rows per CTA, four rows and one key (or
 // one column of V) per thread, 16-byte shared loads; the next tile's rows are read
 // into registers meanwhile.  Exact exponentials (expf), so the result holds fp32
-// accuracy.  Softmax keeps a running maximum and sum per row.
+// accuracy.  Softmax keeps a running maximum and sum per row.  Measured: 12 users, 2
+// heads, up to 50 events over up to 700 18 us (4-byte shared loads, no read-ahead: 28);
+// bound by the barriers between the steps of a tile.
 constexpr int PG32_KEYS = 64;
 constexpr int PG32_ROWS = 16;
 constexpr int PG32_THREADS = 256;
@@ -339,6 +341,13 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
 // streams K, V (TMA, one box per page part, 128B swizzle), key times and the
 // position band (cp.async) through a ring of stages, and never waits for a value it
 // loads: block-table entries come 32 boxes at a time, a batch ahead.
+// Measured (B200, 8 heads, fp16): one event of each of 64 users over 700 .. 4096
+// cached ones 55 us, 5.7 TB/s of K and V (87% of the copy bandwidth); 55 users over 4096,
+// one full round of CTAs, 6.3 TB/s.  One event of one user over 301: 6.5 us, all
+// latency (four dependent loads, then the first tile).  Per-lane copies of times and
+// bands instead of bulk ones, with the producer waiting for its loads: 134 us.
+// Eight warps and 128-key tiles at 2 CTAs per SM: 66 us; 32 rows per CTA (more
+// registers, 2 CTAs per SM): 16 users x 16 events 49 us, with 16 rows 34 us.
 constexpr int PGS_KEYS = 64;  // keys per tile, 16 per warp
 constexpr int PGS_WARPS = 4;
 constexpr int PGS_THREADS = (PGS_WARPS + 1) * 32;
@@ -929,6 +938,11 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
 // at most 128 rows has no second tile: then both halves of the machinery take the
 // same rows and every other key tile each, and their results are added at the end.
 // Softmax takes two passes, the first for each row's maximum and sum.
+// Measured (B200, 8 heads, bf16): 512 events of each of 8 users over 8192 162 us,
+// 411 TFLOP/s (25% of the measured matmul peak; the tensor pipe is 23% active, the
+// schedulers issue in 63% of the cycles, about 11 thread instructions per element).
+// With every event at the same time, so that no time bucket has to be looked up, it
+// takes 141 us.  16 columns at a time (no register spills, twice the loads and votes): 177 us.
 constexpr int PGT_KEYS = 64;
 constexpr int PGT_ROWS = 256;
 constexpr int PGT_STAGES = 6;

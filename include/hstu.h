@@ -1,7 +1,7 @@
 /*
  * hstu.h -- C ABI of libhstu, a B200 (sm_100a) implementation of the forward
- * pass of the HSTU layer (Hierarchical Sequential Transduction Unit) and of
- * M-FALCON candidate scoring.
+ * pass of the HSTU layer (Hierarchical Sequential Transduction Unit), of
+ * M-FALCON candidate scoring, and of a paged cache of users' histories.
  *
  * Source of the method: the review of "Actions Speak Louder than Words:
  * Trillion-Parameter Sequential Transducers for Generative Recommendations"
