@@ -369,6 +369,7 @@ struct PgsSmem {
   static constexpr uint32_t kBars = kMlC + 16 * 8;
   static constexpr uint32_t kAbort = kBars + 2 * PGS_STAGES * 8;
   static constexpr uint32_t kBytes = kAbort + 16 + 1024;           // + align slack
+  static_assert(kMlC - kMl >= 128 * 4, "the lengths that are sorted fit over the maxima");
   static_assert(kSide % 16 == 0 && kSideBytes % 16 == 0, "bulk copies");
   static_assert(PGS_WARPS * 16 * PGS_OLD * 4 <= kSide, "the partial sums fit over the stages");
 };
@@ -499,7 +500,8 @@ hstu_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_kv, const __grid_c
   const int g = static_cast<int>((id / p.H) % p.groups);
   int u = static_cast<int>(id / p.H / p.groups);
   if (p.sorted)
-    u = paged_nth_longest(p, u, reinterpret_cast<int32_t*>(smem), reinterpret_cast<int*>(smem + 1024));
+    u = paged_nth_longest(p, u, reinterpret_cast<int32_t*>(smem + PgsSmem::kMl),
+                          reinterpret_cast<int*>(smem + PgsSmem::kMlC));
   const int warp = warp_id(), lane = lane_id(), tid = threadIdx.x;
   PagedSeq<PGS_KEYS> s;
   const int r0 = g * R;

@@ -500,6 +500,15 @@ class PagedCache:
                       self.lengths.data_ptr())
 
 
+def _ids(ids, n: int, what: str):
+    """Pointer of `n` int32 sequence numbers (None: 0 .. n - 1)."""
+    if ids is None:
+        return None
+    if ids.dtype is not torch.int32 or ids.numel() != n or not ids.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous int32 sequence numbers are needed")
+    return ids.data_ptr()
+
+
 def cache_workspace_bytes(cache: PagedCache, batch: int) -> int:
     return lib().hstu_cache_workspace_bytes(ctypes.byref(cache.c()), batch)
 
@@ -513,7 +522,8 @@ def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), j.batch)
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.kv.device)
-    _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j), _p(seq_ids), _p(workspace),
+    _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j),
+                                    _ids(seq_ids, j.batch, "cache_reserve"), _p(workspace),
                                     workspace.numel(), _stream(stream)), "hstu_cache_reserve")
 
 
@@ -530,9 +540,10 @@ def cache_append(cache: PagedCache, layer: int, chunk: Jagged, k, v, seq_ids=Non
     if k.dtype != cache.kv.dtype or v.dtype != cache.kv.dtype:
         raise ValueError("cache_append: k and v must have the cache's type")
     c, j = cache.c(), chunk.c()
-    _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j), _p(seq_ids), _p(k),
-                                   _rows_ld(k, "k"), _p(v), _rows_ld(v, "v"), _stream(stream)),
-           "hstu_cache_append")
+    _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j),
+                                   _ids(seq_ids, j.batch, "cache_append"), k.data_ptr(),
+                                   _rows_ld(k, "k"), v.data_ptr(), _rows_ld(v, "v"),
+                                   _stream(stream)), "hstu_cache_append")
 
 
 def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=None, stream=None):
@@ -542,7 +553,8 @@ def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=No
     if kv_out is None:
         kv_out = torch.empty((L, total, 2 * H * 64), dtype=cache.kv.dtype, device=cache.kv.device)
     ts = torch.empty(total, dtype=torch.int64, device=cache.kv.device)
-    _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), offsets.numel() - 1, _p(seq_ids),
+    n = offsets.numel() - 1
+    _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), n, _ids(seq_ids, n, "cache_gather"),
                                    _p(offsets), total, _p(kv_out), _p(ts), _stream(stream)),
            "hstu_cache_gather")
     return kv_out, ts
@@ -550,16 +562,17 @@ def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=No
 
 def cache_fork(cache: PagedCache, src_ids, dst_ids, stream=None):
     """dst_ids[i] (an empty sequence) becomes a copy of src_ids[i] sharing its pages."""
-    if src_ids.numel() != dst_ids.numel():
-        raise ValueError("cache_fork: one destination per source")
-    _check(lib().hstu_cache_fork(ctypes.byref(cache.c()), src_ids.numel(), _p(src_ids),
-                                 _p(dst_ids), _stream(stream)), "hstu_cache_fork")
+    n = src_ids.numel()
+    _check(lib().hstu_cache_fork(ctypes.byref(cache.c()), n, _ids(src_ids, n, "cache_fork"),
+                                 _ids(dst_ids, n, "cache_fork"), _stream(stream)),
+           "hstu_cache_fork")
 
 
 def cache_release(cache: PagedCache, seq_ids, window: int = 0, sinks: int = 0, stream=None):
     """Release whole sequences, or with a window the pages that no later event sees."""
-    _check(lib().hstu_cache_release(ctypes.byref(cache.c()), seq_ids.numel(), _p(seq_ids), window,
-                                    sinks, _stream(stream)), "hstu_cache_release")
+    n = seq_ids.numel()
+    _check(lib().hstu_cache_release(ctypes.byref(cache.c()), n, _ids(seq_ids, n, "cache_release"),
+                                    window, sinks, _stream(stream)), "hstu_cache_release")
 
 
 def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tensor:
@@ -580,8 +593,9 @@ def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context,
         raise ValueError(f"{fn}: q must have the cache's type")
     c, ca, j = cfg.c(), cache.c(), chunk.c()
     _check(getattr(lib(), fn)(ctypes.byref(c), ctypes.byref(ca), layer, ctypes.byref(j),
-                              _p(seq_ids), max_context, window, sinks, _p(q), _rows_ld(q, "q"),
-                              _p(rab_pos), _p(rab_time), _p(av_out), _stream(stream)), fn)
+                              _ids(seq_ids, j.batch, fn), max_context, window, sinks, q.data_ptr(),
+                              _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(),
+                              av_out.data_ptr(), _stream(stream)), fn)
     return av_out
 
 
@@ -630,7 +644,7 @@ def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache,
         workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     arr = (LayerWeightsT * L)(*[w.c() for w in weights])
     _check(lib().hstu_extend(ctypes.byref(c), L, arr, ctypes.byref(ca), ctypes.byref(j),
-                             _p(seq_ids), max_context, window, sinks, _p(x_in), _p(y_out),
+                             _ids(seq_ids, j.batch, "extend"), max_context, window, sinks, _p(x_in), _p(y_out),
                              _p(workspace), workspace.numel(), _stream(stream)), "hstu_extend")
     return y_out
 

@@ -170,3 +170,34 @@ def test_bad_calls_are_refused(H):
     assert ext(cache=_cache(H, ref_count=None)) == 1
     assert ext(x=None) == 1
     assert ext(nbytes=100) == 4
+
+
+def test_binding_refuses_wrong_tensors(H):
+    """Layouts that the bare pointers would misread are refused by the handle and the calls."""
+    import torch
+    mk = lambda **kw: H.PagedCache(**{**dict(  # noqa: E731
+        kv=torch.zeros(1, 4, 2, 1, 16, 64, dtype=torch.float16), timestamps=torch.zeros(4, 16, dtype=torch.int64),
+        ref_count=torch.zeros(4, dtype=torch.int32), block_table=torch.zeros(3, 5, dtype=torch.int32),
+        lengths=torch.zeros(3, dtype=torch.int32)), **kw})
+    cache = mk()
+    assert cache.c().num_seqs == 3 and cache.c().max_blocks == 5 and cache.c().dtype == 2
+    for kw in (dict(kv=torch.zeros(4, 2, 1, 16, 64, dtype=torch.float16)),
+               dict(kv=torch.zeros(1, 4, 2, 1, 16, 64, dtype=torch.float64)),
+               dict(kv=torch.zeros(1, 4, 2, 1, 64, 16, dtype=torch.float16).transpose(4, 5)),
+               dict(timestamps=torch.zeros(4, 16, dtype=torch.int32)), dict(timestamps=torch.zeros(16, 4, dtype=torch.int64)),
+               dict(ref_count=torch.zeros(5, dtype=torch.int32)), dict(lengths=torch.zeros(3, dtype=torch.int64)),
+               dict(block_table=torch.zeros(4, 5, dtype=torch.int32)), dict(block_table=torch.zeros(5, 3, dtype=torch.int32).t())):
+        with pytest.raises(ValueError):
+            mk(**kw)
+    with pytest.raises(ValueError):
+        H.cache_release(cache, torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        H.cache_fork(cache, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    chunk = H.Jagged(torch.zeros(2, dtype=torch.int64), torch.zeros(1, dtype=torch.int64), 1, 1)
+    rows = torch.zeros(1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        H.cache_append(cache, 0, chunk, rows.to(torch.bfloat16), rows)
+    with pytest.raises(ValueError):
+        H.cache_append(cache, 0, chunk, rows.t(), rows)
+    with pytest.raises(ValueError):
+        H.cache_append(cache, 0, chunk, rows, rows, seq_ids=torch.zeros(2, dtype=torch.int32))

@@ -548,3 +548,78 @@ def test_captured_and_on_another_stream(H):
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(out, want) and torch.equal(out_w, want_w)
     assert H.device_status() == 0
+
+
+def test_extend_captured_and_replayed(H):
+    """One captured extension, replayed: every replay appends the next events."""
+    case = make_case("small-bf16", seed=14, lengths=[60, 33])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    mk = dict(layers=case.cfg.num_layers, heads=case.cfg.num_heads, pages=30, seqs=2, blocks=9, ps=16, dtype="fp16")
+    eager, graphed = nan_cache(H, **mk), nan_cache(H, **mk)
+    first = chunk_of(H, [60, 33], case.timestamps)
+    later = int(max(case.timestamps)) + 100
+    x = t["x"][:5].contiguous()
+    ts = [torch.tensor([later + 10 * k + i for i in range(5)], dtype=torch.int64, device="cuda") for k in range(3)]
+    want = []
+    H.extend(cfg, weights, eager, first, t["x"], 100)
+    for k in range(3):
+        want.append(H.extend(cfg, weights, eager, H.Jagged(chunk_of(H, [3, 2], ts[k].tolist()).offsets, ts[k], 3, 5), x, 100))
+    H.extend(cfg, weights, graphed, first, t["x"], 100)
+    buf = ts[0].clone()
+    j = H.Jagged(chunk_of(H, [3, 2], [0] * 5).offsets, buf, 3, 5)
+    y = torch.empty_like(want[0])
+    ws = torch.empty(H.extend_workspace_bytes(cfg, graphed, 2, 5), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        H.extend(cfg, weights, graphed, j, x, 100, y_out=y, workspace=ws)
+    for k in range(3):
+        buf.copy_(ts[k])
+        g.replay()
+        assert torch.equal(y, want[k]), k
+    assert H.device_status() == 0
+    assert tables(eager) == tables(graphed) and graphed.lengths.tolist() == [69, 39]
+
+
+def test_two_streams_read_one_cache(H):
+    ac = make_attn_case([900, 400, 77], 4, 64, 64, seed=9, dtype="bf16")
+    cache = nan_cache(H, layers=1, heads=4, pages=50, seqs=3, blocks=16, ps=64, dtype="bf16")
+    j, rows = load_cache(H, ac, cache, [200, 1, 30])
+    cfg = H.LayerConfig(256, 4, 64, 64, dtype="bf16")
+    rp, rt = tensor(ac.rab_pos, torch.float32, "cuda"), tensor(ac.rab_time, torch.float32, "cuda")
+    q = tensor(ac.q[rows], torch.bfloat16, "cuda")
+    kw = [{}, dict(window=50, sinks=5)]
+    want = [H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, 900, **k) for k in kw]
+    out = [torch.zeros_like(want[0]) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, o, k in zip(streams, out, kw):
+            H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, 900, av_out=o, stream=st, **k)
+    torch.cuda.synchronize()
+    assert H.device_status() == 0
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_many_heads_and_wide_spans(H):
+    """16 heads, one position bucket, and times at the largest span the kernels take."""
+    run_attn(H, [(130, 1), (70, 9), (300, 60)], 16, "fp16", "silu", 16, Pb=1, Tb=256)
+    for dtype, c in (("fp16", 3), ("fp16", 200), ("fp32", 3)):
+        ac = make_attn_case([250], 1, 16, 128, seed=2, dtype=dtype)
+        for span, want_status in ((2 ** 31 - 4, 0), (2 ** 31 + 5, 6)):
+            ac.timestamps[:] = 1_700_000_000 + span
+            ac.timestamps[0] = 1_700_000_000
+            cache = nan_cache(H, layers=1, heads=1, pages=20, seqs=1, blocks=16, ps=16, dtype=dtype)
+            j, rows = load_cache(H, ac, cache, [c])
+            cfg = H.LayerConfig(64, 1, 16, 128, dtype=dtype)
+            got = H.paged_attn_fwd(cfg, cache, 0, j, tensor(ac.q[rows], DT[dtype], "cuda"),
+                                   tensor(ac.rab_pos, torch.float32, "cuda"),
+                                   tensor(ac.rab_time, torch.float32, "cuda"), 250)
+            assert H.device_status() == want_status, (dtype, c, span)
+            if want_status == 0:
+                f = np.float64
+                want = P.chunk_attention(ac.q[250 - c:].astype(f), ac.k.astype(f), ac.v.astype(f), ac.timestamps,
+                                         ac.rab_pos.astype(f), ac.rab_time.astype(f), 1)
+                assert_close(got.float().cpu().numpy(), want, f"span {span} {dtype}", scaled=True)
