@@ -455,9 +455,11 @@ def stochastic_length(jag: Jagged, alpha: float, seed: int, step: int, x=None, s
 _CACHE_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
-@dataclass
+@dataclass(frozen=True)
 class PagedCache:
-    """A paged history cache: the caller's five device tensors (see hstu_cache_t)."""
+    """A paged history cache: the caller's five device tensors (see hstu_cache_t).
+    The handle checks their layout and keeps their addresses: make another one for
+    other tensors."""
     kv: torch.Tensor           # [L, num_pages, 2, H, page_size, 64], the cache type
     timestamps: torch.Tensor   # int64 [num_pages, page_size]
     ref_count: torch.Tensor    # int32 [num_pages]
@@ -492,12 +494,12 @@ class PagedCache:
                              "timestamps int64 [pages, page], ref_count int32 [pages], "
                              "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous")
 
+        object.__setattr__(self, "_c", CacheT(
+            ks[0], ks[3], _CACHE_DTYPE[kv.dtype], ks[4], ks[1], bs[0], bs[1], kv.data_ptr(),
+            ts.data_ptr(), self.ref_count.data_ptr(), table.data_ptr(), self.lengths.data_ptr()))
+
     def c(self) -> CacheT:
-        L, pages, _, H, ps, _ = self.kv.shape
-        return CacheT(L, H, _CACHE_DTYPE[self.kv.dtype], ps, pages, self.lengths.shape[0],
-                      self.block_table.shape[1], self.kv.data_ptr(), self.timestamps.data_ptr(),
-                      self.ref_count.data_ptr(), self.block_table.data_ptr(),
-                      self.lengths.data_ptr())
+        return self._c
 
 
 def _ids(ids, n: int, what: str):
@@ -589,13 +591,15 @@ def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tenso
 
 def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context, window, sinks,
                 seq_ids, av_out, stream):
-    if q.dtype != cache.kv.dtype:
+    if q.dtype is not cache.kv.dtype:
         raise ValueError(f"{fn}: q must have the cache's type")
-    c, ca, j = cfg.c(), cache.c(), chunk.c()
-    _check(getattr(lib(), fn)(ctypes.byref(c), ctypes.byref(ca), layer, ctypes.byref(j),
-                              _ids(seq_ids, j.batch, fn), max_context, window, sinks, q.data_ptr(),
-                              _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(),
-                              av_out.data_ptr(), _stream(stream)), fn)
+    c, j = cfg.c(), chunk.c()
+    status = getattr(lib(), fn)(
+        ctypes.byref(c), ctypes.byref(cache._c), layer, ctypes.byref(j),
+        None if seq_ids is None else _ids(seq_ids, j.batch, fn), max_context, window, sinks,
+        q.data_ptr(), _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(), av_out.data_ptr(),
+        _stream(stream))
+    _check(status, fn)
     return av_out
 
 
