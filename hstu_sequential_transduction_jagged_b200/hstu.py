@@ -591,8 +591,8 @@ def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tenso
 
 def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context, window, sinks,
                 seq_ids, av_out, stream):
-    if q.dtype is not cache.kv.dtype:
-        raise ValueError(f"{fn}: q must have the cache's type")
+    if q.dtype is not cache.kv.dtype or q.shape != (chunk.total_tokens, cfg.num_heads * 64):
+        raise ValueError(f"{fn}: q must be [total_tokens, num_heads * 64] in the cache's type")
     c, j = cfg.c(), chunk.c()
     status = getattr(lib(), fn)(
         ctypes.byref(c), ctypes.byref(cache._c), layer, ctypes.byref(j),
@@ -609,9 +609,8 @@ def paged_attn_fwd(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagge
     """Eq. 2 for the chunk's rows (the last events of their sequences) over the
     cache: AV [T, H*64] in cfg dtype.  window > 0: a row sees the last `window`
     events up to itself and the first `sinks` events of its sequence."""
-    if av_out is None:
-        av_out = torch.empty((chunk.total_tokens, cfg.num_heads * cfg.dv), dtype=cfg.torch_dtype,
-                             device=q.device)
+    if av_out is None:  # q's shape and type
+        av_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     return _paged_attn("hstu_paged_attn_fwd", cfg, cache, layer, chunk, q, rab_pos, rab_time,
                        max_context, window, sinks, seq_ids, av_out, stream)
 
