@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -455,16 +456,34 @@ def stochastic_length(jag: Jagged, alpha: float, seed: int, step: int, x=None, s
 _CACHE_DTYPE = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
 
 
-@dataclass(frozen=True)
-class PagedCache:
+class PagedCache(namedtuple("PagedCache", "kv timestamps ref_count block_table lengths desc")):
     """A paged history cache: the caller's five device tensors (see hstu_cache_t).
+      kv           [L, num_pages, 2, H, page_size, 64], the cache type
+      timestamps   int64 [num_pages, page_size]
+      ref_count    int32 [num_pages]
+      block_table  int32 [num_seqs, max_blocks], -1 = no page
+      lengths      int32 [num_seqs]
     The handle checks their layout and keeps their addresses: make another one for
     other tensors."""
-    kv: torch.Tensor           # [L, num_pages, 2, H, page_size, 64], the cache type
-    timestamps: torch.Tensor   # int64 [num_pages, page_size]
-    ref_count: torch.Tensor    # int32 [num_pages]
-    block_table: torch.Tensor  # int32 [num_seqs, max_blocks], -1 = no page
-    lengths: torch.Tensor      # int32 [num_seqs]
+    __slots__ = ()
+
+    def __new__(cls, kv, timestamps, ref_count, block_table, lengths):
+        # the calls hand bare pointers on, so the layout is checked here
+        ks, bs, i32 = kv.shape, block_table.shape, torch.int32
+        dtype = _CACHE_DTYPE.get(kv.dtype)
+        if not (dtype is not None and len(ks) == 6 and ks[2] == 2 and ks[5] == 64
+                and timestamps.shape == (ks[1], ks[4]) and timestamps.dtype is torch.int64
+                and ref_count.shape == (ks[1],) and len(bs) == 2 and lengths.shape == (bs[0],)
+                and ref_count.dtype is i32 and block_table.dtype is i32 and lengths.dtype is i32
+                and kv.is_contiguous() and timestamps.is_contiguous()
+                and block_table.is_contiguous() and ref_count.is_contiguous()
+                and lengths.is_contiguous()):
+            raise ValueError("PagedCache: kv [L, pages, 2, H, page, 64] (fp16, bf16 or fp32), "
+                             "timestamps int64 [pages, page], ref_count int32 [pages], "
+                             "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous")
+        return super().__new__(cls, kv, timestamps, ref_count, block_table, lengths, CacheT(
+            ks[0], ks[3], dtype, ks[4], ks[1], bs[0], bs[1], kv.data_ptr(), timestamps.data_ptr(),
+            ref_count.data_ptr(), block_table.data_ptr(), lengths.data_ptr()))
 
     @staticmethod
     def empty(num_layers: int, num_heads: int, num_pages: int, num_seqs: int, max_blocks: int,
@@ -479,27 +498,8 @@ class PagedCache:
             torch.zeros(num_pages, **i32), torch.full((num_seqs, max_blocks), -1, **i32),
             torch.zeros(num_seqs, **i32))
 
-    def __post_init__(self):
-        # the calls hand bare pointers on, so the layout is checked here
-        kv, ts, table = self.kv, self.timestamps, self.block_table
-        ks, bs = kv.shape, table.shape
-        if not (len(ks) == 6 and ks[2] == 2 and ks[5] == 64 and kv.dtype in _CACHE_DTYPE
-                and ts.shape == (ks[1], ks[4]) and ts.dtype == torch.int64
-                and self.ref_count.shape == (ks[1],) and len(bs) == 2
-                and self.lengths.shape == (bs[0],) and self.ref_count.dtype == torch.int32
-                and table.dtype == torch.int32 and self.lengths.dtype == torch.int32
-                and kv.is_contiguous() and ts.is_contiguous() and table.is_contiguous()
-                and self.ref_count.is_contiguous() and self.lengths.is_contiguous()):
-            raise ValueError("PagedCache: kv [L, pages, 2, H, page, 64] (fp16, bf16 or fp32), "
-                             "timestamps int64 [pages, page], ref_count int32 [pages], "
-                             "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous")
-
-        object.__setattr__(self, "_c", CacheT(
-            ks[0], ks[3], _CACHE_DTYPE[kv.dtype], ks[4], ks[1], bs[0], bs[1], kv.data_ptr(),
-            ts.data_ptr(), self.ref_count.data_ptr(), table.data_ptr(), self.lengths.data_ptr()))
-
     def c(self) -> CacheT:
-        return self._c
+        return self.desc
 
 
 def _ids(ids, n: int, what: str):
@@ -595,7 +595,7 @@ def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context,
         raise ValueError(f"{fn}: q must be [total_tokens, num_heads * 64] in the cache's type")
     c, j = cfg.c(), chunk.c()
     status = getattr(lib(), fn)(
-        ctypes.byref(c), ctypes.byref(cache._c), layer, ctypes.byref(j),
+        ctypes.byref(c), ctypes.byref(cache.desc), layer, ctypes.byref(j),
         None if seq_ids is None else _ids(seq_ids, j.batch, fn), max_context, window, sinks,
         q.data_ptr(), _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(), av_out.data_ptr(),
         _stream(stream))
