@@ -460,6 +460,28 @@ def test_extend_follows_the_oracle(H, name, kw):
         assert_close(y.cpu().numpy(), np.concatenate(want), f"extend {name} {phi2} {kw} step {step}")
 
 
+def test_extend_with_long_chunks(H):
+    """Fresh histories through the stack on the many-rows kernel (and its LayerNorm
+    partial sums): the rows of hstu_forward, up to the roundings of both."""
+    case = make_case("small-bf16", seed=15, lengths=[300, 129, 512, 257, 400, 64] * 3)
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    jag = H.Jagged(t["offsets"], t["timestamps"], case.max_len, case.total_tokens)
+    cache = nan_cache(H, layers=case.cfg.num_layers, heads=4, pages=200, seqs=18, blocks=9, ps=64, dtype="fp16")
+    H.profiler_start()
+    y = H.extend(cfg, weights, cache, jag, t["x"], 512)
+    assert "paged_attention_tile" in H.profiler_stop()
+    assert H.device_status() == 0
+    dense = torch.empty((case.cfg.num_layers, case.total_tokens, 512), dtype=torch.float16, device="cuda")
+    z = H.forward(cfg, weights, jag, t["x"], kv_cache_out=dense)
+    assert_close(y.cpu().numpy(), z.cpu().numpy(), "extend from nothing against forward")
+    kv, _ = H.cache_gather(cache, t["offsets"], case.total_tokens)
+    assert torch.equal(kv[0], dense[0])
+    want, _ = O.forward(case.x, case.offsets, case.timestamps, case.layers, case.cfg)
+    assert_close(y.cpu().numpy(), want, "extend from nothing against the oracle")
+
+
 def test_serving_round(H):
     """A request as a server makes it: encode a history, keep it in pages, branch
     it, extend the branches, score candidates over one of them; every part
