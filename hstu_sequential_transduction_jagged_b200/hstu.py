@@ -256,10 +256,25 @@ def mfalcon_workspace_bytes(cfg: LayerConfig, num_cand: int) -> int:
     return lib().hstu_mfalcon_workspace_bytes(ctypes.byref(c), num_cand)
 
 
-def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor]):
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """A new tensor for a call on `stream` (None: the current one).  It comes from that
+    stream's memory: a block of another stream's may still be in use by work pending
+    there, and may be handed out again, once dropped, before the call has run.  A
+    result that the current stream goes on to use is kept for that stream too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if current != stream:
+        t.record_stream(current)
+    return t
+
+
+def _workspace(nbytes: int, device, workspace: Optional[torch.Tensor], stream=None):
     if workspace is not None:
         return workspace
-    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return _empty(max(nbytes, 1), torch.uint8, device, stream)
 
 
 def attn_fwd(cfg: LayerConfig, jag: Jagged, q, k, v, rab_pos, rab_time, av_out=None,
@@ -332,7 +347,7 @@ def layer_bwd(cfg: LayerConfig, w: "LayerWeights", jag: Jagged, x_in, dy, x_res=
            "dbeta": torch.empty(hv, **f32) if w.ln_beta is not None else None}
     g = LayerGradsT(*[None if out[n] is None else out[n].data_ptr() for n in
                       ("dw1", "db1", "dw2", "db2", "drab_pos", "drab_time", "dgamma", "dbeta")])
-    ws = _workspace(layer_bwd_workspace_bytes(cfg, T), dev, workspace)
+    ws = _workspace(layer_bwd_workspace_bytes(cfg, T), dev, workspace, stream)
     c, j, wc = cfg.c(), jag.c(), w.c()
     _check(lib().hstu_layer_bwd(ctypes.byref(c), ctypes.byref(wc), ctypes.byref(j), _p(x_in),
                                 _p(x_res), _p(dy), _p(out["dx"]), ctypes.byref(g), _p(ws),
@@ -365,7 +380,7 @@ def layer_fwd(cfg: LayerConfig, w: LayerWeights, jag: Jagged, x_in, x_res=None, 
     if y_out is None:
         y_out = torch.empty((jag.total_tokens, cfg.d_model), dtype=torch.float32, device=dev)
     nbytes = layer_workspace_bytes(cfg, jag.total_tokens)
-    ws = _workspace(nbytes, dev, workspace)
+    ws = _workspace(nbytes, dev, workspace, stream)
     c, j, wc = cfg.c(), jag.c(), w.c()
     _check(lib().hstu_layer_fwd(ctypes.byref(c), ctypes.byref(wc), ctypes.byref(j), _p(x_in),
                                 _p(x_res), _p(y_out), _p(y_out_lp), _p(kv_cache_out), _p(ws),
@@ -398,7 +413,7 @@ def forward(cfg: LayerConfig, weights: Sequence[LayerWeights], jag: Jagged, x_in
     L = len(weights)
     if y_out is None:
         y_out = torch.empty((jag.total_tokens, cfg.d_model), dtype=torch.float32, device=dev)
-    ws = _workspace(forward_workspace_bytes(cfg, L, jag.total_tokens), dev, workspace)
+    ws = _workspace(forward_workspace_bytes(cfg, L, jag.total_tokens), dev, workspace, stream)
     arr = (LayerWeightsT * L)(*[w.c() for w in weights])
     c, j = cfg.c(), jag.c()
     _check(lib().hstu_forward(ctypes.byref(c), L, arr, ctypes.byref(j), _p(x_in), _p(y_out),
@@ -417,7 +432,7 @@ def mfalcon_score(cfg: LayerConfig, weights: Sequence[LayerWeights], history: Ja
     L = len(weights)
     if scores is None:
         scores = torch.empty(M, dtype=torch.float32, device=dev)
-    ws = _workspace(mfalcon_workspace_bytes(cfg, M), dev, workspace)
+    ws = _workspace(mfalcon_workspace_bytes(cfg, M), dev, workspace, stream)
     arr = (LayerWeightsT * L)(*[w.c() for w in weights])
     c, j = cfg.c(), history.c()
     _check(lib().mfalcon_score(ctypes.byref(c), L, arr, ctypes.byref(j), _p(kv_cache),
@@ -523,7 +538,7 @@ def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None
     c, j = cache.c(), chunk.c()
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), j.batch)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.kv.device)
+        workspace = _workspace(nbytes, cache.kv.device, None, stream)
     _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j),
                                     _ids(seq_ids, j.batch, "cache_reserve"), _p(workspace),
                                     workspace.numel(), _stream(stream)), "hstu_cache_reserve")
@@ -553,8 +568,8 @@ def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=No
     layout of forward()'s kv_cache_out, timestamps [total])."""
     L, _, _, H, _, _ = cache.kv.shape
     if kv_out is None:
-        kv_out = torch.empty((L, total, 2 * H * 64), dtype=cache.kv.dtype, device=cache.kv.device)
-    ts = torch.empty(total, dtype=torch.int64, device=cache.kv.device)
+        kv_out = _empty((L, total, 2 * H * 64), cache.kv.dtype, cache.kv.device, stream)
+    ts = _empty(total, torch.int64, cache.kv.device, stream)
     n = offsets.numel() - 1
     _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), n, _ids(seq_ids, n, "cache_gather"),
                                    _p(offsets), total, _p(kv_out), _p(ts), _stream(stream)),
@@ -579,11 +594,11 @@ def cache_release(cache: PagedCache, seq_ids, window: int = 0, sinks: int = 0, s
 
 def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tensor:
     """Move the used pages into the lowest ids; returns their number (int32 [1], device)."""
-    live = torch.empty(1, dtype=torch.int32, device=cache.kv.device)
+    live = _empty(1, torch.int32, cache.kv.device, stream)
     c = cache.c()
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), 0)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=cache.kv.device)
+        workspace = _workspace(nbytes, cache.kv.device, None, stream)
     _check(lib().hstu_cache_compact(ctypes.byref(c), _p(live), _p(workspace), workspace.numel(),
                                     _stream(stream)), "hstu_cache_compact")
     return live
@@ -609,8 +624,10 @@ def paged_attn_fwd(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagge
     """Eq. 2 for the chunk's rows (the last events of their sequences) over the
     cache: AV [T, H*64] in cfg dtype.  window > 0: a row sees the last `window`
     events up to itself and the first `sinks` events of its sequence."""
-    if av_out is None:  # q's shape and type
+    if av_out is None and stream is None:  # q's shape and type
         av_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif av_out is None:
+        av_out = _empty(q.shape, q.dtype, q.device, stream)
     return _paged_attn("hstu_paged_attn_fwd", cfg, cache, layer, chunk, q, rab_pos, rab_time,
                        max_context, window, sinks, seq_ids, av_out, stream)
 
@@ -620,8 +637,7 @@ def paged_attn_fwd_f32(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: J
                        av_out=None, stream=None) -> torch.Tensor:
     """paged_attn_fwd with the result in fp32."""
     if av_out is None:
-        av_out = torch.empty((chunk.total_tokens, cfg.num_heads * cfg.dv), dtype=torch.float32,
-                             device=q.device)
+        av_out = _empty((chunk.total_tokens, cfg.num_heads * cfg.dv), torch.float32, q.device, stream)
     return _paged_attn("hstu_paged_attn_fwd_f32", cfg, cache, layer, chunk, q, rab_pos, rab_time,
                        max_context, window, sinks, seq_ids, av_out, stream)
 
@@ -639,12 +655,12 @@ def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache,
     dev = x_in.device
     L = len(weights)
     if y_out is None:
-        y_out = torch.empty((chunk.total_tokens, cfg.d_model), dtype=torch.float32, device=dev)
+        y_out = _empty((chunk.total_tokens, cfg.d_model), torch.float32, dev, stream)
     c, ca, j = cfg.c(), cache.c(), chunk.c()
     if workspace is None:
         nbytes = lib().hstu_extend_workspace_bytes(ctypes.byref(c), ctypes.byref(ca), j.batch,
                                                    j.total_tokens)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        workspace = _workspace(nbytes, dev, None, stream)
     arr = (LayerWeightsT * L)(*[w.c() for w in weights])
     _check(lib().hstu_extend(ctypes.byref(c), L, arr, ctypes.byref(ca), ctypes.byref(j),
                              _ids(seq_ids, j.batch, "extend"), max_context, window, sinks, _p(x_in), _p(y_out),

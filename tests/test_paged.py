@@ -201,3 +201,37 @@ def test_binding_refuses_wrong_tensors(H):
         H.cache_append(cache, 0, chunk, rows.t(), rows)
     with pytest.raises(ValueError):
         H.cache_append(cache, 0, chunk, rows, rows, seq_ids=torch.zeros(2, dtype=torch.int32))
+
+
+def test_memory_of_a_call_comes_from_its_stream(H, monkeypatch):
+    """Workspaces and results of a call on another stream are made on that stream, and the
+    current one, which takes the result, is named to the allocator."""
+    import contextlib
+    import types
+    log, now = [], ["current"]
+
+    class Block:
+        def record_stream(self, s):
+            log.append(("kept for", s))
+
+    @contextlib.contextmanager
+    def on(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def empty(shape, dtype, device):
+        log.append(("made on", now[-1], shape))
+        return Block()
+
+    fake = types.SimpleNamespace(empty=empty, uint8="u8", cuda=types.SimpleNamespace(
+        current_stream=lambda: now[-1], stream=on))
+    monkeypatch.setattr(H, "torch", fake)
+    H._workspace(5, "cuda", None, "side")
+    assert log == [("made on", "side", 5), ("kept for", "current")]
+    del log[:]
+    H._empty(7, "f32", "cuda", "current")
+    H._empty(8, "f32", "cuda")
+    assert log == [("made on", "current", 7), ("made on", "current", 8)]
+    given = Block()
+    assert H._workspace(5, "cuda", given, "side") is given and len(log) == 2

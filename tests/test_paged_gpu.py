@@ -645,3 +645,65 @@ def test_many_heads_and_wide_spans(H):
                 want = P.chunk_attention(ac.q[250 - c:].astype(f), ac.k.astype(f), ac.v.astype(f), ac.timestamps,
                                          ac.rab_pos.astype(f), ac.rab_time.astype(f), 1)
                 assert_close(got.float().cpu().numpy(), want, f"span {span} {dtype}", scaled=True)
+
+
+def test_default_memory_on_side_streams(H, monkeypatch):
+    """Two caches that reserve, extend, gather and compact on two streams at once, with
+    workspaces and results of the calls' own making: all of it from the calls' streams, and
+    the results of the same calls made one after the other."""
+    case = make_case("small-bf16", seed=21, lengths=[90, 40])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    jag = H.Jagged(t["offsets"], t["timestamps"], case.max_len, case.total_tokens)
+    later = int(max(case.timestamps)) + 10
+    more = [chunk_of(H, [k + 1, 3], [later + 5 * k + i for i in range(k + 1)] + [later + 5 * k + i for i in range(3)])
+            for k in range(4)]
+    # caches start with a sequence that is released, so that compact has pages to move
+    mk = dict(layers=case.cfg.num_layers, heads=case.cfg.num_heads, pages=40, seqs=3, blocks=9, ps=16, dtype="fp16")
+    first = chunk_of(H, [33], range(33))
+    total = case.total_tokens + sum(m.total_tokens for m in more)
+    ends = [int(n) + sum(int(m.offsets[u + 1] - m.offsets[u]) for m in more) for u, n in enumerate((90, 40))]
+    off = tensor(np.array([0, ends[0], ends[0] + ends[1]]), torch.int64, "cuda")
+
+    def life(cache, stream):
+        out = []
+        H.cache_reserve(cache, first, seq_ids=two, stream=stream)
+        for l in range(case.cfg.num_layers):
+            H.cache_append(cache, l, first, zeros, zeros, seq_ids=two, stream=stream)
+        out.append(H.extend(cfg, weights, cache, jag, t["x"], 200, stream=stream))
+        H.cache_release(cache, two, stream=stream)
+        for m in more:
+            out.append(H.extend(cfg, weights, cache, m, t["x"][:m.total_tokens].contiguous(), 200, stream=stream))
+        out.append(H.cache_compact(cache, stream=stream))
+        out += H.cache_gather(cache, off, total, stream=stream)
+        return out
+
+    two = i32([2])
+    zeros = torch.zeros((33, case.cfg.num_heads * 64), dtype=torch.float16, device="cuda")
+    want = life(nan_cache(H, **mk), None)
+    caches, streams = [nan_cache(H, **mk) for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    made, empty = [], torch.empty
+
+    def watched(*a, **kw):
+        made.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    for _ in range(3):
+        got = []
+        for c, s in zip(caches, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            del made[:]
+            monkeypatch.setattr(torch, "empty", watched)
+            got.append(life(c, s))
+            monkeypatch.setattr(torch, "empty", empty)
+            assert len(made) >= 13 and all(m == s for m in made)
+        torch.cuda.synchronize()
+        assert H.device_status() == 0
+        for g in got:
+            assert len(g) == len(want)
+            for a, b in zip(g, want):
+                assert torch.equal(a, b)
+        for c in caches:
+            H.cache_release(c, i32(range(3)))
