@@ -492,10 +492,12 @@ class PagedCache(namedtuple("PagedCache", "kv timestamps ref_count block_table l
                 and ref_count.dtype is i32 and block_table.dtype is i32 and lengths.dtype is i32
                 and kv.is_contiguous() and timestamps.is_contiguous()
                 and block_table.is_contiguous() and ref_count.is_contiguous()
-                and lengths.is_contiguous()):
+                and lengths.is_contiguous() and timestamps.get_device() == kv.get_device()
+                == ref_count.get_device() == block_table.get_device() == lengths.get_device()):
             raise ValueError("PagedCache: kv [L, pages, 2, H, page, 64] (fp16, bf16 or fp32), "
                              "timestamps int64 [pages, page], ref_count int32 [pages], "
-                             "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous")
+                             "block_table int32 [seqs, blocks] and lengths int32 [seqs], contiguous, "
+                             "on one device")
         return super().__new__(cls, kv, timestamps, ref_count, block_table, lengths, CacheT(
             ks[0], ks[3], dtype, ks[4], ks[1], bs[0], bs[1], kv.data_ptr(), timestamps.data_ptr(),
             ref_count.data_ptr(), block_table.data_ptr(), lengths.data_ptr()))
@@ -526,6 +528,40 @@ def _ids(ids, n: int, what: str):
     return ids.data_ptr()
 
 
+def _cache_stream(cache: PagedCache, stream, what: str, *tensors) -> int:
+    """The raw stream of a call on `cache`, which is launched on the current GPU: the cache
+    and the other tensors (None: not given) have to be there."""
+    dev = cache.kv.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what}: the cache is not on the current GPU")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: a tensor is not on the cache's GPU")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"{what}: the stream is not the cache's GPU's")
+    return stream.cuda_stream
+
+
+def _chunk(chunk: Jagged, what: str) -> JaggedT:
+    """The chunk's C description."""
+    o, t, i64 = chunk.offsets, chunk.timestamps, torch.int64
+    total, rows, seg = chunk.total_tokens, t.numel(), chunk.segments
+    if not (o.dtype is i64 and t.dtype is i64 and rows >= total and o.is_contiguous()
+            and t.is_contiguous()):
+        raise ValueError(f"{what}: the chunk needs contiguous int64 offsets and int64 timestamps "
+                         "of total_tokens rows")
+    return JaggedT(o.numel() - 1, total, chunk.max_len, o.data_ptr(), t.data_ptr() if rows else None,
+                   None if seg is None else seg.data_ptr(), chunk.max_static)
+
+
+def _dense(t: torch.Tensor, shape, dtype, what: str, name: str):
+    """A contiguous tensor of a shape and type."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be contiguous, {list(shape)} {dtype}")
+
+
 def cache_workspace_bytes(cache: PagedCache, batch: int) -> int:
     return lib().hstu_cache_workspace_bytes(ctypes.byref(cache.c()), batch)
 
@@ -535,13 +571,14 @@ def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None
     sequence) and lengthen the sequences; shared partial last pages are copied.
     A pool that is too small leaves everything as it was and is reported in
     device_status()."""
-    c, j = cache.c(), chunk.c()
+    c, j = cache.c(), _chunk(chunk, "cache_reserve")
+    ids = _ids(seq_ids, j.batch, "cache_reserve")
+    raw = _cache_stream(cache, stream, "cache_reserve", chunk.offsets, chunk.timestamps, seq_ids, workspace)
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), j.batch)
         workspace = _workspace(nbytes, cache.kv.device, None, stream)
-    _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j),
-                                    _ids(seq_ids, j.batch, "cache_reserve"), _p(workspace),
-                                    workspace.numel(), _stream(stream)), "hstu_cache_reserve")
+    _check(lib().hstu_cache_reserve(ctypes.byref(c), ctypes.byref(j), ids, _p(workspace),
+                                    workspace.numel(), raw), "hstu_cache_reserve")
 
 
 def _rows_ld(t: torch.Tensor, what: str) -> int:
@@ -554,66 +591,90 @@ def _rows_ld(t: torch.Tensor, what: str) -> int:
 
 def cache_append(cache: PagedCache, layer: int, chunk: Jagged, k, v, seq_ids=None, stream=None):
     """Write K and V ([T, H*64], any row stride) of the chunk's rows into a layer's pages."""
-    if k.dtype != cache.kv.dtype or v.dtype != cache.kv.dtype:
-        raise ValueError("cache_append: k and v must have the cache's type")
-    c, j = cache.c(), chunk.c()
-    _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j),
-                                   _ids(seq_ids, j.batch, "cache_append"), k.data_ptr(),
-                                   _rows_ld(k, "k"), v.data_ptr(), _rows_ld(v, "v"),
-                                   _stream(stream)), "hstu_cache_append")
+    dtype, rows = cache.kv.dtype, (chunk.total_tokens, cache.desc.num_heads * 64)
+    if k.dtype is not dtype or v.dtype is not dtype or k.shape != rows or v.shape != rows:
+        raise ValueError("cache_append: k and v must be [total_tokens, num_heads * 64] in the cache's type")
+    c, j = cache.c(), _chunk(chunk, "cache_append")
+    ids = _ids(seq_ids, j.batch, "cache_append")
+    raw = _cache_stream(cache, stream, "cache_append", k, v, chunk.offsets, chunk.timestamps, seq_ids)
+    _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j), ids, k.data_ptr(),
+                                   _rows_ld(k, "k"), v.data_ptr(), _rows_ld(v, "v"), raw),
+           "hstu_cache_append")
 
 
 def cache_gather(cache: PagedCache, offsets, total: int, seq_ids=None, kv_out=None, stream=None):
     """Whole sequences out of their pages: returns (kv [L, total, 2*H*64] in the
     layout of forward()'s kv_cache_out, timestamps [total])."""
     L, _, _, H, _, _ = cache.kv.shape
+    n = offsets.numel() - 1
+    if offsets.dtype is not torch.int64 or not offsets.is_contiguous():
+        raise ValueError("cache_gather: offsets must be contiguous int64")
+    if kv_out is not None:
+        _dense(kv_out, (L, total, 2 * H * 64), cache.kv.dtype, "cache_gather", "kv_out")
+    ids = _ids(seq_ids, n, "cache_gather")
+    raw = _cache_stream(cache, stream, "cache_gather", offsets, seq_ids, kv_out)
     if kv_out is None:
         kv_out = _empty((L, total, 2 * H * 64), cache.kv.dtype, cache.kv.device, stream)
     ts = _empty(total, torch.int64, cache.kv.device, stream)
-    n = offsets.numel() - 1
-    _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), n, _ids(seq_ids, n, "cache_gather"),
-                                   _p(offsets), total, _p(kv_out), _p(ts), _stream(stream)),
-           "hstu_cache_gather")
+    _check(lib().hstu_cache_gather(ctypes.byref(cache.c()), n, ids, _p(offsets), total, _p(kv_out),
+                                   _p(ts), raw), "hstu_cache_gather")
     return kv_out, ts
 
 
 def cache_fork(cache: PagedCache, src_ids, dst_ids, stream=None):
     """dst_ids[i] (an empty sequence) becomes a copy of src_ids[i] sharing its pages."""
     n = src_ids.numel()
-    _check(lib().hstu_cache_fork(ctypes.byref(cache.c()), n, _ids(src_ids, n, "cache_fork"),
-                                 _ids(dst_ids, n, "cache_fork"), _stream(stream)),
-           "hstu_cache_fork")
+    src, dst = _ids(src_ids, n, "cache_fork"), _ids(dst_ids, n, "cache_fork")
+    raw = _cache_stream(cache, stream, "cache_fork", src_ids, dst_ids)
+    _check(lib().hstu_cache_fork(ctypes.byref(cache.c()), n, src, dst, raw), "hstu_cache_fork")
 
 
 def cache_release(cache: PagedCache, seq_ids, window: int = 0, sinks: int = 0, stream=None):
     """Release whole sequences, or with a window the pages that no later event sees."""
     n = seq_ids.numel()
-    _check(lib().hstu_cache_release(ctypes.byref(cache.c()), n, _ids(seq_ids, n, "cache_release"),
-                                    window, sinks, _stream(stream)), "hstu_cache_release")
+    ids = _ids(seq_ids, n, "cache_release")
+    raw = _cache_stream(cache, stream, "cache_release", seq_ids)
+    _check(lib().hstu_cache_release(ctypes.byref(cache.c()), n, ids, window, sinks, raw),
+           "hstu_cache_release")
 
 
 def cache_compact(cache: PagedCache, workspace=None, stream=None) -> torch.Tensor:
     """Move the used pages into the lowest ids; returns their number (int32 [1], device)."""
+    raw = _cache_stream(cache, stream, "cache_compact", workspace)
     live = _empty(1, torch.int32, cache.kv.device, stream)
     c = cache.c()
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), 0)
         workspace = _workspace(nbytes, cache.kv.device, None, stream)
-    _check(lib().hstu_cache_compact(ctypes.byref(c), _p(live), _p(workspace), workspace.numel(),
-                                    _stream(stream)), "hstu_cache_compact")
+    _check(lib().hstu_cache_compact(ctypes.byref(c), _p(live), _p(workspace), workspace.numel(), raw),
+           "hstu_cache_compact")
     return live
 
 
 def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context, window, sinks,
-                seq_ids, av_out, stream):
-    if q.dtype is not cache.kv.dtype or q.shape != (chunk.total_tokens, cfg.num_heads * 64):
+                seq_ids, av_out, out_dtype, stream):
+    kv, heads = cache.kv, cfg.num_heads
+    rows = (chunk.total_tokens, heads * 64)
+    if q.dtype is not kv.dtype or q.shape != rows:
         raise ValueError(f"{fn}: q must be [total_tokens, num_heads * 64] in the cache's type")
-    c, j = cfg.c(), chunk.c()
+    f32 = torch.float32
+    _dense(rab_pos, (heads, cfg.num_pos_buckets), f32, fn, "rab_pos")
+    _dense(rab_time, (heads, cfg.num_time_buckets), f32, fn, "rab_time")
+    if av_out is not None:
+        _dense(av_out, rows, out_dtype, fn, "av_out")
+    c, j = cfg.c(), _chunk(chunk, fn)
+    ids = None if seq_ids is None else _ids(seq_ids, j.batch, fn)
+    raw = _cache_stream(cache, stream, fn, q, rab_pos, rab_time, chunk.offsets, chunk.timestamps,
+                        seq_ids, av_out)
+    if av_out is None:
+        if stream is None and out_dtype is q.dtype:  # less host work than a shape and a device
+            av_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            av_out = _empty(rows, out_dtype, q.device, stream)
     status = getattr(lib(), fn)(
-        ctypes.byref(c), ctypes.byref(cache.desc), layer, ctypes.byref(j),
-        None if seq_ids is None else _ids(seq_ids, j.batch, fn), max_context, window, sinks,
-        q.data_ptr(), _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(), av_out.data_ptr(),
-        _stream(stream))
+        ctypes.byref(c), ctypes.byref(cache.desc), layer, ctypes.byref(j), ids, max_context, window,
+        sinks, q.data_ptr(), _rows_ld(q, "q"), rab_pos.data_ptr(), rab_time.data_ptr(),
+        av_out.data_ptr(), raw)
     _check(status, fn)
     return av_out
 
@@ -624,22 +685,16 @@ def paged_attn_fwd(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagge
     """Eq. 2 for the chunk's rows (the last events of their sequences) over the
     cache: AV [T, H*64] in cfg dtype.  window > 0: a row sees the last `window`
     events up to itself and the first `sinks` events of its sequence."""
-    if av_out is None and stream is None:  # q's shape and type
-        av_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    elif av_out is None:
-        av_out = _empty(q.shape, q.dtype, q.device, stream)
     return _paged_attn("hstu_paged_attn_fwd", cfg, cache, layer, chunk, q, rab_pos, rab_time,
-                       max_context, window, sinks, seq_ids, av_out, stream)
+                       max_context, window, sinks, seq_ids, av_out, cache.kv.dtype, stream)
 
 
 def paged_attn_fwd_f32(cfg: LayerConfig, cache: PagedCache, layer: int, chunk: Jagged, q, rab_pos,
                        rab_time, max_context: int, window: int = 0, sinks: int = 0, seq_ids=None,
                        av_out=None, stream=None) -> torch.Tensor:
     """paged_attn_fwd with the result in fp32."""
-    if av_out is None:
-        av_out = _empty((chunk.total_tokens, cfg.num_heads * cfg.dv), torch.float32, q.device, stream)
     return _paged_attn("hstu_paged_attn_fwd_f32", cfg, cache, layer, chunk, q, rab_pos, rab_time,
-                       max_context, window, sinks, seq_ids, av_out, stream)
+                       max_context, window, sinks, seq_ids, av_out, torch.float32, stream)
 
 
 def extend_workspace_bytes(cfg: LayerConfig, cache: PagedCache, batch: int, total_tokens: int) -> int:
@@ -654,17 +709,24 @@ def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache,
     append, paged attention, f2); returns Y [T, d] fp32."""
     dev = x_in.device
     L = len(weights)
+    rows = (chunk.total_tokens, cfg.d_model)
+    _dense(x_in, rows, cfg.torch_dtype, "extend", "x_in")
+    if y_out is not None:
+        _dense(y_out, rows, torch.float32, "extend", "y_out")
+    c, ca, j = cfg.c(), cache.c(), _chunk(chunk, "extend")
+    ids = _ids(seq_ids, j.batch, "extend")
+    raw = _cache_stream(cache, stream, "extend", x_in, chunk.offsets, chunk.timestamps, seq_ids,
+                        y_out, workspace)
     if y_out is None:
-        y_out = _empty((chunk.total_tokens, cfg.d_model), torch.float32, dev, stream)
-    c, ca, j = cfg.c(), cache.c(), chunk.c()
+        y_out = _empty(rows, torch.float32, dev, stream)
     if workspace is None:
         nbytes = lib().hstu_extend_workspace_bytes(ctypes.byref(c), ctypes.byref(ca), j.batch,
                                                    j.total_tokens)
         workspace = _workspace(nbytes, dev, None, stream)
     arr = (LayerWeightsT * L)(*[w.c() for w in weights])
     _check(lib().hstu_extend(ctypes.byref(c), L, arr, ctypes.byref(ca), ctypes.byref(j),
-                             _ids(seq_ids, j.batch, "extend"), max_context, window, sinks, _p(x_in), _p(y_out),
-                             _p(workspace), workspace.numel(), _stream(stream)), "hstu_extend")
+                             ids, max_context, window, sinks, _p(x_in), _p(y_out), _p(workspace),
+                             workspace.numel(), raw), "hstu_extend")
     return y_out
 
 

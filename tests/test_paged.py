@@ -235,3 +235,78 @@ def test_memory_of_a_call_comes_from_its_stream(H, monkeypatch):
     assert log == [("made on", "current", 7), ("made on", "current", 8)]
     given = Block()
     assert H._workspace(5, "cuda", given, "side") is given and len(log) == 2
+
+
+def test_binding_refuses_what_pointers_would_misread(H):
+    """Rows, tables, offsets and results of the wrong size, type or layout; tensors that are not on
+    the GPU.  Everything is refused before the library is called."""
+    import torch
+    f16, f32, i32, i64 = torch.float16, torch.float32, torch.int32, torch.int64
+    z = lambda *s, dtype=f16: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    cache = H.PagedCache(z(2, 4, 2, 3, 16, 64), z(4, 16, dtype=i64), z(4, dtype=i32), z(3, 5, dtype=i32), z(3, dtype=i32))
+    T, hv = 6, 192
+    chunk = H.Jagged(torch.tensor([0, 2, 6]), z(T, dtype=i64), 4, T)
+    ids = z(2, dtype=i32)
+    rows = z(T, hv)
+    bad_chunks = [H.Jagged(chunk.offsets.to(i32), chunk.timestamps, 4, T),
+                  H.Jagged(z(6, dtype=i64)[::2], chunk.timestamps, 4, T),
+                  H.Jagged(chunk.offsets, chunk.timestamps[:-1], 4, T),
+                  H.Jagged(chunk.offsets, chunk.timestamps.to(i32), 4, T),
+                  H.Jagged(chunk.offsets, z(2 * T, dtype=i64)[::2], 4, T)]
+    bad_rows = [z(T - 1, hv), z(T + 1, hv), z(T, hv - 64), z(T, 2 * hv)[:, :hv - 64], z(T, 3, 64), z(T, hv, dtype=torch.bfloat16)]
+
+    def refused(match, f, *a, **kw):
+        with pytest.raises(ValueError, match=match):
+            f(*a, **kw)
+
+    # append
+    for bad in bad_rows:
+        refused("total_tokens, num_heads", H.cache_append, cache, 0, chunk, bad, rows, seq_ids=ids)
+        refused("total_tokens, num_heads", H.cache_append, cache, 0, chunk, rows, bad, seq_ids=ids)
+    # attention
+    cfg = H.LayerConfig(hv, 3, 16, 32, dtype="fp16")
+    rp, rt = z(3, 16, dtype=f32), z(3, 32, dtype=f32)
+
+    def attn(fn=H.paged_attn_fwd, q=rows, rp=rp, rt=rt, chunk=chunk, **kw):
+        return fn(cfg, cache, 0, chunk, q, rp, rt, 20, **kw)
+
+    for fn in (H.paged_attn_fwd, H.paged_attn_fwd_f32):
+        for bad in bad_rows:
+            refused("q must be", attn, fn, q=bad)
+        for bad in (z(3, 15, dtype=f32), z(2, 16, dtype=f32), z(16, dtype=f32), z(3, 16), z(3, 16, dtype=torch.float64),
+                    z(16, 3, dtype=f32).t()):
+            refused("rab_pos", attn, fn, rp=bad)
+        for bad in (z(3, 16, dtype=f32), z(3, 32), z(3, 64, dtype=f32)[:, ::2]):
+            refused("rab_time", attn, fn, rt=bad)
+    for bad in bad_rows[:2] + [z(T, hv, dtype=f32), z(hv, T).t(), z(T, 2 * hv)[:, :hv]]:
+        refused("av_out", attn, av_out=bad)
+    refused("av_out", attn, H.paged_attn_fwd_f32, av_out=rows)
+    # extend (a fp32 stack keeps its cache in fp32)
+    cache32 = H.PagedCache(cache.kv.float(), *cache[1:5])
+    ecfg = H.LayerConfig(128, 3, 16, 32, dtype="fp32")
+    w = [H.LayerWeights(*[z(4, dtype=f32)] * 6)] * 2
+    x = z(T, 128, dtype=f32)
+
+    def ext(x=x, chunk=chunk, **kw):
+        return H.extend(ecfg, w, cache32, chunk, x, 20, **kw)
+
+    for bad in (x[:-1], z(T, 64, dtype=f32), z(T, 256, dtype=f32)[:, :128], z(128, T, dtype=f32).t(), x.half(), x.bfloat16()):
+        refused("x_in", ext, bad)
+        refused("y_out", ext, y_out=bad)
+    # gather
+    off = torch.tensor([0, 5, 9])
+    for bad in (off.to(i32), z(6, dtype=i64)[::2]):
+        refused("offsets", H.cache_gather, cache, bad, 9)
+    for bad in (z(2, 8, 2 * hv), z(1, 9, 2 * hv), z(2, 9, 2 * hv, dtype=f32), z(2, 9, 4 * hv)[:, :, ::2]):
+        refused("kv_out", H.cache_gather, cache, off, 9, kv_out=bad)
+    for bad in bad_chunks:
+        refused("the chunk needs", H.cache_reserve, cache, bad, seq_ids=ids)
+        refused("the chunk needs", H.cache_append, cache, 0, bad, rows, rows, seq_ids=ids)
+        refused("the chunk needs", attn, chunk=bad, seq_ids=ids)
+        refused("the chunk needs", ext, chunk=bad, seq_ids=ids)
+    # nothing wrong but that the tensors are on the CPU
+    for f in (lambda: H.cache_reserve(cache, chunk, seq_ids=ids), lambda: H.cache_append(cache, 0, chunk, rows, rows),
+              lambda: H.cache_gather(cache, off, 9), lambda: H.cache_fork(cache, ids, ids),
+              lambda: H.cache_release(cache, ids), lambda: H.cache_compact(cache), attn, ext,
+              lambda: attn(H.paged_attn_fwd_f32)):
+        refused("not on the current GPU", f)

@@ -707,3 +707,40 @@ def test_default_memory_on_side_streams(H, monkeypatch):
                 assert torch.equal(a, b)
         for c in caches:
             H.cache_release(c, i32(range(3)))
+
+
+def test_tensors_elsewhere_are_refused(H):
+    """Tensors of the call that are not on the cache's GPU, and parts of a cache that are not."""
+    ac = make_attn_case([40, 20], 1, 16, 16, seed=5, dtype="fp16")
+    cache = nan_cache(H, layers=1, heads=1, pages=12, seqs=4, blocks=4, ps=16, dtype="fp16")
+    j, rows = load_cache(H, ac, cache, [3, 2])
+    x = tensor(ac.k[rows], torch.float16, "cuda")
+    rp = torch.zeros((1, 16), device="cuda")
+    cfg = H.LayerConfig(64, 1, 16, 16, dtype="fp16")
+    ids = i32([0, 1])
+    off = tensor(np.array([0, 40, 60]), torch.int64, "cuda")
+    far = H.Jagged(j.offsets.cpu(), j.timestamps, j.max_len, j.total_tokens)
+    old = H.Jagged(j.offsets, j.timestamps.cpu(), j.max_len, j.total_tokens)
+    ws = torch.empty(1 << 16, dtype=torch.uint8)
+
+    def attn(q=x, rp=rp, rt=rp, chunk=j, **kw):
+        return H.paged_attn_fwd(cfg, cache, 0, chunk, q, rp, rt, 40, **kw)
+
+    for f in (lambda: H.cache_append(cache, 0, j, x.cpu(), x), lambda: H.cache_append(cache, 0, j, x, x.cpu()),
+              lambda: H.cache_append(cache, 0, far, x, x), lambda: H.cache_append(cache, 0, j, x, x, seq_ids=ids.cpu()),
+              lambda: H.cache_reserve(cache, far), lambda: H.cache_reserve(cache, old),
+              lambda: H.cache_reserve(cache, j, seq_ids=ids.cpu()), lambda: H.cache_reserve(cache, j, workspace=ws),
+              lambda: H.cache_compact(cache, workspace=ws), lambda: H.cache_gather(cache, off.cpu(), 60),
+              lambda: H.cache_gather(cache, off, 60, kv_out=torch.empty(1, 60, 128, dtype=torch.float16)),
+              lambda: H.cache_fork(cache, ids.cpu(), i32([2, 3])), lambda: H.cache_fork(cache, ids, i32([2, 3]).cpu()),
+              lambda: H.cache_release(cache, ids.cpu()), lambda: attn(q=x.cpu()), lambda: attn(rp=rp.cpu()),
+              lambda: attn(rt=rp.cpu()), lambda: attn(chunk=far), lambda: attn(chunk=old), lambda: attn(seq_ids=ids.cpu()),
+              lambda: attn(av_out=torch.empty_like(x, device="cpu"))):
+        with pytest.raises(ValueError, match="not on the cache's GPU"):
+            f()
+    for n in range(5):
+        parts = list(cache[:5])
+        parts[n] = parts[n].cpu()
+        with pytest.raises(ValueError, match="on one device"):
+            H.PagedCache(*parts)
+    assert H.device_status() == 0 and cache.lengths.tolist() == [40, 20, 0, 0]
