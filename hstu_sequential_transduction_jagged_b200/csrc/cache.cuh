@@ -35,7 +35,10 @@ struct CacheView {
   int32_t L, num_pages, H, ps_log2, max_blocks, num_seqs, elt;
 
   __device__ __forceinline__ int ps() const { return 1 << ps_log2; }
-  __device__ __forceinline__ int blocks(int n) const { return (n + ps() - 1) >> ps_log2; }
+  // of any n >= 0: n + ps - 1 would overflow at the top
+  __device__ __forceinline__ int blocks(int n) const {
+    return (n >> ps_log2) + ((n & (ps() - 1)) != 0 ? 1 : 0);
+  }
   __device__ __forceinline__ int64_t page_bytes() const {  // of one layer
     return (static_cast<int64_t>(2 * H) << ps_log2) * 64 * elt;
   }
@@ -533,7 +536,7 @@ hstu_cache_gather_kernel(const CacheView c, const int32_t* __restrict__ seq_ids,
   if (cnt == 0) return;
   const bool seq_ok = static_cast<uint32_t>(seq) < static_cast<uint32_t>(c.num_seqs);
   const int n = seq_ok ? c.lengths[seq] : -1;
-  if (cnt != n || o0 < 0 || o1 > total || c.blocks(n) > c.max_blocks) {
+  if (cnt < 0 || cnt != n || o0 < 0 || o1 > total || c.blocks(n) > c.max_blocks) {
     if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) record_status(HSTU_ERR_DEVICE_CHECK);
     return;
   }

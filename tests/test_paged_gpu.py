@@ -744,3 +744,28 @@ def test_tensors_elsewhere_are_refused(H):
         with pytest.raises(ValueError, match="on one device"):
             H.PagedCache(*parts)
     assert H.device_status() == 0 and cache.lengths.tolist() == [40, 20, 0, 0]
+
+
+@pytest.mark.parametrize("ps", [16, 128])
+def test_lengths_that_no_table_holds(H, ps):
+    """Lengths at the top of their type: reported, nothing read past the block table."""
+    cache = nan_cache(H, layers=1, heads=1, pages=12, seqs=4, blocks=4, ps=ps, dtype="fp16")
+    H.cache_reserve(cache, chunk_of(H, [20, 20], range(40)))
+    x = torch.zeros((3, 64), dtype=torch.float16, device="cuda")
+    j, one = chunk_of(H, [3], range(3)), i32([0])
+    off = tensor(np.array([0, 3]), torch.int64, "cuda")
+    down = tensor(np.array([3, 2]), torch.int64, "cuda")
+    cfg = H.LayerConfig(64, 1, 16, 16, dtype="fp16")
+    rp = torch.zeros((1, 16), device="cuda")
+    for n in (2 ** 31 - 1, 2 ** 31 - ps, 2 ** 31 - ps - 1, 4 * ps + 1):
+        cache.lengths[0] = n
+        before = [t.clone() for t in cache[:5]]
+        for call in (lambda: H.cache_append(cache, 0, j, x, x), lambda: H.cache_gather(cache, off, 3),
+                     lambda: H.cache_fork(cache, one, i32([2])), lambda: H.cache_release(cache, one),
+                     lambda: H.cache_release(cache, one, window=7), lambda: H.cache_reserve(cache, j),
+                     lambda: H.cache_gather(cache, down, 3, seq_ids=i32([-1])),
+                     lambda: H.paged_attn_fwd(cfg, cache, 0, j, x, rp, rp, 2 ** 31 - 1)):
+            call()
+            assert H.device_status() == 6, n
+            for a, b in zip(before, cache[:5]):
+                assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
