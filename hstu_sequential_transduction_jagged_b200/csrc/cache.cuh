@@ -55,6 +55,9 @@ struct CacheView {
 
 constexpr int CACHE_META_THREADS = 1024;
 constexpr int CACHE_COPY_THREADS = 256;
+// Seconds between a visible event and the last one, at most: the attention kernels work
+// on int32 times.
+constexpr int32_t CACHE_MAX_SPAN = INT32_MAX - 2;
 constexpr int CACHE_UNIT_V = 2048;  // 16-byte vectors that a block of compact moves at a time
 
 // Exclusive prefix sum of one value per thread over a 1024-thread CTA; `total`
@@ -97,17 +100,26 @@ struct ReserveWs {
   int32_t* pages;   // [num_pages] ids handed out, in order
 };
 
+// What the attention of the same call (hstu_extend) will need of the sequences.
+struct ReserveSeen {
+  int max_context;            // the longest one it is sized for
+  int window, sinks;
+  const int64_t* timestamps;  // of the new events; nullptr: no attention follows
+};
+
 // One CTA: decides the whole reservation, then makes it, or changes nothing.
 // Users in batch order; a user takes the copy of its shared partial last page
 // first, then its new blocks in order.  A sequence named twice, one out of range,
-// a block table too short and a pool without enough free pages are reported.
+// a block table too short and a pool without enough free pages are reported; so is,
+// where attention follows, what that would report: it would run into it after the
+// lengths have grown, and later layers would append what it did not compute.
 __global__ void __launch_bounds__(CACHE_META_THREADS)
 hstu_cache_reserve_kernel(const CacheView c, int B, const int32_t* __restrict__ seq_ids,
                           const int64_t* __restrict__ offsets, int64_t total_new, int max_new,
-                          const ReserveWs ws) {
+                          const ReserveSeen seen, const ReserveWs ws) {
   __shared__ int sWarp[33];
   __shared__ int sBad;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = lane_id();
   if (tid == 0) sBad = 0;
   __syncthreads();
   // what each user needs; the sign bit of lengths[] marks a sequence as taken by
@@ -126,7 +138,8 @@ hstu_cache_reserve_kernel(const CacheView c, int B, const int32_t* __restrict__ 
         if (n < 0) n = -1;  // named twice
         const int64_t cnt = o1 - o0;
         bad = n < 0 || o0 < 0 || cnt < 0 || cnt > max_new || o1 > total_new ||
-              n + cnt > (static_cast<int64_t>(c.max_blocks) << c.ps_log2);
+              n + cnt > (static_cast<int64_t>(c.max_blocks) << c.ps_log2) ||
+              (cnt > 0 && n + cnt > seen.max_context);
         if (!bad) {
           const int have = c.blocks(n), want = c.blocks(n + static_cast<int>(cnt));
           need = want - have;
@@ -157,6 +170,35 @@ hstu_cache_reserve_kernel(const CacheView c, int B, const int32_t* __restrict__ 
     base = sBad ? 0 : base + total;
   }
   const int want_pages = base;
+  // the earlier events that the new rows see: their pages exist, and the earliest is not
+  // too long before the last event (a warp per user)
+  if (seen.timestamps != nullptr && !sBad) {
+    bool missing = false;
+    for (int u = warp_id(); u < B; u += CACHE_META_THREADS / 32) {
+      const int64_t o0 = offsets[u], o1 = offsets[u + 1];
+      if (o1 == o0) continue;
+      const int n = ws.old_len[u];
+      const int32_t* row = c.row(seq_ids != nullptr ? seq_ids[u] : u);
+      const int lo = seen.window > 0 ? max(0, n - seen.window + 1) : 0;  // at most n
+      const int sink_end = min(seen.window > 0 ? seen.sinks : 0, lo);
+      const int b0 = lo >> c.ps_log2, n_sink = min(c.blocks(sink_end), b0);
+      const int nb = n_sink + c.blocks(n) - b0;
+#pragma unroll 4
+      for (int i = lane; i < nb; i += 32) missing |= !c.page_ok(row[i < n_sink ? i : b0 + (i - n_sink)]);
+      if (lane == 0) {
+        const int first = sink_end > 0 ? 0 : lo;
+        int64_t t = seen.timestamps[o0];
+        if (first < n) {
+          const int page = row[first >> c.ps_log2];
+          if (c.page_ok(page)) t = c.ts[(static_cast<int64_t>(page) << c.ps_log2) + (first & (c.ps() - 1))];
+        }
+        missing |= seen.timestamps[o1 - 1] - t > CACHE_MAX_SPAN;
+      }
+    }
+    __syncthreads();  // sBad has been read
+    if (missing) sBad = 1;
+    __syncthreads();
+  }
   // the lowest free page ids
   if (!sBad) {
     int found = 0;
@@ -189,7 +231,6 @@ hstu_cache_reserve_kernel(const CacheView c, int B, const int32_t* __restrict__ 
   }
   // hand out: a thread per user for its first pages, the warp for the rest of a long one
   constexpr int OWN = 4;
-  const int lane = lane_id();
   for (int u0 = 0; u0 < B; u0 += CACHE_META_THREADS) {
     const int u = u0 + tid;
     const bool in = u < B;

@@ -980,12 +980,23 @@ ReserveWs carve_reserve(const hstu_cache_t*, int32_t batch, void* ws) {
   return r;
 }
 
+struct PagedJob {
+  const hstu_cache_t* cache;
+  const hstu_jagged_t* chunk;
+  const int32_t* seq_ids;
+  int32_t max_context, window, sinks;
+  const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
+};
+
+// `attn`: the attention of the same call, or nullptr.
 hstu_status_t launch_reserve(const hstu_cache_t* c, const hstu_jagged_t* chunk, const int32_t* seq_ids,
-                             const ReserveWs& ws, cudaStream_t st) {
+                             const PagedJob* attn, const ReserveWs& ws, cudaStream_t st) {
   const CacheView v = view_of(c);
+  const ReserveSeen seen = attn != nullptr ? ReserveSeen{attn->max_context, attn->window, attn->sinks, chunk->timestamps}
+                                           : ReserveSeen{INT32_MAX, 0, 0, nullptr};
   ProfScope prof(K_CACHE_META, st);
   hstu_cache_reserve_kernel<<<1, CACHE_META_THREADS, 0, st>>>(v, chunk->batch, seq_ids, chunk->offsets,
-                                                              chunk->total_tokens, chunk->max_len, ws);
+                                                              chunk->total_tokens, chunk->max_len, seen, ws);
   HSTU_CHECK_CUDA(cudaGetLastError());
   const dim3 grid(chunk->batch, c->num_layers + 1);
   hstu_cache_reserve_rows_kernel<<<grid, CACHE_COPY_THREADS, 0, st>>>(v, seq_ids, chunk->offsets,
@@ -1017,14 +1028,6 @@ hstu_status_t launch_append(const hstu_cache_t* c, int layer, const hstu_jagged_
   HSTU_CHECK_CUDA(cudaGetLastError());
   return HSTU_OK;
 }
-
-struct PagedJob {
-  const hstu_cache_t* cache;
-  const hstu_jagged_t* chunk;
-  const int32_t* seq_ids;
-  int32_t max_context, window, sinks;
-  const int32_t* go;  // the reservation's verdict (hstu_extend), or nullptr
-};
 
 // Whether the many-rows kernel is the faster one, by what a CTA of each kernel takes
 // (microseconds on B200): a start and an end of 5 (rows) or 9 (tile), and per key tile
@@ -2065,7 +2068,7 @@ hstu_status_t hstu_cache_reserve(const hstu_cache_t* cache, const hstu_jagged_t*
   if (!aligned16(workspace)) return HSTU_ERR_INVALID_ARGUMENT;
   if (workspace == nullptr || ws_bytes < cache_ws_bytes(cache, chunk->batch))
     return HSTU_ERR_WORKSPACE_TOO_SMALL;
-  return launch_reserve(cache, chunk, seq_ids, carve_reserve(cache, chunk->batch, workspace),
+  return launch_reserve(cache, chunk, seq_ids, nullptr, carve_reserve(cache, chunk->batch, workspace),
                         static_cast<cudaStream_t>(stream));
 }
 
@@ -2265,8 +2268,8 @@ hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
   void* yl[2] = {sp + 2 * fbytes, sp + 2 * fbytes + lbytes};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const ReserveWs rws = carve_reserve(cache, chunk->batch, sp + stream_ws_bytes(cfg, T));
-  if ((s = launch_reserve(cache, chunk, seq_ids, rws, st)) != HSTU_OK) return s;
   const PagedJob pj{cache, chunk, seq_ids, max_context, window, sinks, rws.state};
+  if ((s = launch_reserve(cache, chunk, seq_ids, &pj, rws, st)) != HSTU_OK) return s;
   AttnJob base;
   std::memset(&base, 0, sizeof(base));
   base.cfg = cfg;

@@ -23,6 +23,7 @@
 #include <cooperative_groups.h>
 
 #include "attn.cuh"
+#include "cache.cuh"
 
 namespace hstu {
 
@@ -121,7 +122,7 @@ __device__ __forceinline__ int paged_nth_longest(const PagedParams& p, int u, in
 }
 
 // Seconds relative to the last event, shifted into [0, 2^31 - 3].
-constexpr int32_t PG_T0 = INT32_MAX - 2;
+constexpr int32_t PG_T0 = CACHE_MAX_SPAN;
 __device__ __forceinline__ int32_t paged_rel(int64_t t, int64_t t_last) {
   const int64_t d = t - t_last + PG_T0;
   return d < 0 ? 0 : (d > PG_T0 ? PG_T0 : static_cast<int32_t>(d));

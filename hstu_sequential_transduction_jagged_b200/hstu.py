@@ -706,7 +706,9 @@ def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache,
            x_in, max_context: int, window: int = 0, sinks: int = 0, seq_ids=None, y_out=None,
            workspace=None, stream=None) -> torch.Tensor:
     """New events through the stack against the cache (reserve, then per layer f1,
-    append, paged attention, f2); returns Y [T, d] fp32."""
+    append, paged attention, f2); returns Y [T, d] fp32.  A pool that is too small, a
+    sequence that would pass max_context or a missing page that a new row sees leaves the
+    cache as it was and is reported in device_status()."""
     dev = x_in.device
     L = len(weights)
     rows = (chunk.total_tokens, cfg.d_model)

@@ -492,7 +492,10 @@ size_t hstu_extend_workspace_bytes(const hstu_layer_cfg_t* cfg, const hstu_cache
  * Norm removes that scale up to ln_eps).
  *   cache        num_layers = the stack's; dtype fp16 for bf16 layers, fp32 for fp32
  *   x_in         device [T, d] in cfg dtype, y_out device [T, d] fp32
- * When the reservation fails the cache is unchanged and y_out is unspecified. */
+ * All or nothing, as hstu_cache_reserve: also when a sequence would pass max_context, when
+ * an earlier event that a new row sees has no page or lies too long before the last one (see
+ * hstu_paged_attn_fwd).  Then HSTU_ERR_DEVICE_CHECK is recorded, the cache is unchanged
+ * and y_out is unspecified. */
 hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
                           const hstu_layer_weights_t* weights, const hstu_cache_t* cache,
                           const hstu_jagged_t* chunk, const int32_t* seq_ids, int32_t max_context,

@@ -769,3 +769,103 @@ def test_lengths_that_no_table_holds(H, ps):
             assert H.device_status() == 6, n
             for a, b in zip(before, cache[:5]):
                 assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+def unchanged_by(cache, H, call):
+    """The call is reported and leaves the cache as it was."""
+    before = [t.clone() for t in cache[:5]]
+    call()
+    assert H.device_status() == 6
+    for a, b in zip(before, cache[:5]):
+        assert torch.equal(torch.nan_to_num(a), torch.nan_to_num(b))
+
+
+@pytest.mark.parametrize("name", ["small-bf16", "tiny-fp32"])
+def test_extend_refuses_before_it_changes_anything(H, name):
+    """What the attention of an extension would run into is refused with the reservation."""
+    case = make_case(make_case(name).cfg.replace(num_layers=2), seed=22, lengths=[70, 41])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    cache = nan_cache(H, layers=2, heads=case.cfg.num_heads, pages=24, seqs=3, blocks=9, ps=16,
+                      dtype="fp32" if name == "tiny-fp32" else "fp16")
+    H.extend(cfg, weights, cache, H.Jagged(t["offsets"], t["timestamps"], 70, 111), t["x"], 70)
+    assert H.device_status() == 0
+    start = [int(case.timestamps[u]) for u in (0, 70)]
+    last = int(max(case.timestamps)) + 5
+    x = t["x"][:7].contiguous()
+
+    def ext(ts=None, ctx=75, cnt=(5, 2), **kw):
+        ts = [last + i for i in range(sum(cnt))] if ts is None else ts
+        return H.extend(cfg, weights, cache, chunk_of(H, cnt, ts), x[:sum(cnt)], ctx, **kw)
+
+    unchanged_by(cache, H, lambda: ext(ctx=74))              # user 0 would have 75 events
+    unchanged_by(cache, H, lambda: ext(ctx=1))
+    # a visible event just too long ago, of either user; at the border it is taken (below)
+    far = start[0] + 2 ** 31 - 2
+    unchanged_by(cache, H, lambda: ext([far - 4 + i for i in range(5)] + [last, last + 1]))
+    far = start[1] + 2 ** 31 - 2
+    unchanged_by(cache, H, lambda: ext([last + i for i in range(5)] + [far - 1, far]))
+    # pages that fell out of a window of 20 with 17 sinks: user 0 keeps blocks 0, 1 and 3, 4
+    H.cache_release(cache, i32([0]), window=20, sinks=17)
+    assert H.device_status() == 0 and (cache.block_table[0, :5] >= 0).tolist() == [True, True, False, True, True]
+    unchanged_by(cache, H, ext)
+    unchanged_by(cache, H, lambda: ext(window=24))           # the first new row sees event 47
+    unchanged_by(cache, H, lambda: ext(window=20, sinks=33))  # and event 32
+    unchanged_by(cache, H, lambda: ext(window=20, sinks=17, ctx=74))
+    ext(window=23, sinks=32)                                 # events 48 .., and 0 .. 31
+    assert H.device_status() == 0 and cache.lengths.tolist() == [75, 43, 0]
+    # out of the window it does not matter how long ago an event was
+    far = start[1] + 2 ** 31 - 3
+    ext([far], cnt=(0, 1), ctx=200)
+    assert H.device_status() == 0 and cache.lengths.tolist() == [75, 44, 0]
+    unchanged_by(cache, H, lambda: ext([far + 1], cnt=(0, 1), ctx=200))
+    ext([far + 1], cnt=(0, 1), ctx=200, window=1)
+    ext([far + 2 ** 33], cnt=(0, 1), ctx=200, window=1)
+    assert H.device_status() == 0 and cache.lengths.tolist() == [75, 46, 0]
+
+
+def test_extend_refuses_what_its_attention_would_report(H):
+    """Many sequences of many pages, some of them missing here and there: the extension's verdict
+    is that of the attention alone over a copy of the cache."""
+    rng = np.random.default_rng(23)
+    heads, users, ps, blocks = 1, 70, 16, 90
+    dev = dict(device="cuda", dtype=torch.float32)
+    cfg = H.LayerConfig(64, heads, 32, 32, dtype="fp32")
+    weights = [H.LayerWeights(0.05 * torch.randn(256, 64, **dev), torch.zeros(256, **dev), 0.05 * torch.randn(64, 64, **dev),
+                              torch.zeros(64, **dev), torch.zeros(1, 32, **dev), torch.zeros(1, 32, **dev))]
+    verdicts = []
+    for trial in range(24):
+        n = [int(v) for v in rng.integers(0, blocks * ps - 40, users)]
+        cnt = [int(v) for v in rng.integers(0, 4, users)]
+        caches = [nan_cache(H, layers=1, heads=heads, pages=8000, seqs=users, blocks=blocks, ps=ps, dtype="fp32")
+                  for _ in range(2)]
+        window, sinks = (0, 0) if trial % 4 == 0 else (int(rng.integers(1, 300)), int(rng.integers(0, 100)))
+        first = chunk_of(H, n, np.concatenate([np.arange(v) for v in n]))
+        j = chunk_of(H, cnt, np.concatenate([v + np.arange(c) for v, c in zip(n, cnt)]))
+        x = torch.randn(j.total_tokens, 64, **dev)
+        drop = rng.random((users, blocks)) < (0.0 if trial % 3 == 2 else 0.0007)
+        gone = torch.from_numpy(drop).cuda()
+        for c in caches:
+            c.kv.zero_()
+            H.cache_reserve(c, first)
+            if trial % 3:  # what fell out of the window goes
+                H.cache_release(c, i32(range(users)), window=max(window, 1), sinks=sinks)
+            # a page that another sequence's block is in could not be missing: whole pages, last ones not
+            last = torch.tensor([max(0, -(-v // ps) - 1) for v in n], device="cuda")
+            hole = gone & (torch.arange(blocks, device="cuda")[None, :] < last[:, None])
+            c.block_table[hole] = -1
+        assert H.device_status() == 0
+        ctx = max(a + b for a, b in zip(n, cnt))
+        H.cache_reserve(caches[1], j)
+        assert H.device_status() == 0
+        H.paged_attn_fwd(cfg, caches[1], 0, j, x, weights[0].rab_pos, weights[0].rab_time, ctx, window=window, sinks=sinks)
+        want = H.device_status()
+        if want:
+            unchanged_by(caches[0], H, lambda: H.extend(cfg, weights, caches[0], j, x, ctx, window=window, sinks=sinks))
+        else:
+            H.extend(cfg, weights, caches[0], j, x, ctx, window=window, sinks=sinks)
+            assert H.device_status() == 0
+            assert caches[0].lengths.tolist() == [a + b for a, b in zip(n, cnt)]
+        verdicts.append(want)
+    assert 6 <= verdicts.count(6) <= 18, verdicts
