@@ -1071,7 +1071,6 @@ int paged_splits(int64_t ctas, int64_t slots, int max_tiles) {
 template <class Fn, class... Args>
 hstu_status_t launch_cluster(Fn fn, int64_t ctas, int ns, int threads, size_t smem, cudaStream_t st,
                              Args... args) {
-  if (ctas * ns > (int64_t(1) << 31) - 1) return HSTU_ERR_UNSUPPORTED;
   cudaLaunchConfig_t lc;
   std::memset(&lc, 0, sizeof(lc));
   lc.gridDim = dim3(static_cast<unsigned>(ctas * ns));
@@ -1089,6 +1088,60 @@ hstu_status_t launch_cluster(Fn fn, int64_t ctas, int ns, int threads, size_t sm
   return HSTU_OK;
 }
 
+// How a call's attention is launched.
+struct PagedPlan {
+  KernelKind kernel;     // K_PAGED_ROWS, K_PAGED_TILE or K_PAGED_F32
+  int32_t max_context, sinks;
+  int mh;                // 8-row halves per CTA (rows)
+  int groups, nsplit;
+  int64_t ctas;          // before the split
+};
+
+// Refuses a call whose grid would be too large, so that hstu_extend can ask before it
+// reserves.
+hstu_status_t plan_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, int sm_count, PagedPlan* out) {
+  const hstu_cache_t* ca = j.cache;
+  PagedPlan p;
+  p.max_context = static_cast<int32_t>(
+      std::min<int64_t>(j.max_context, static_cast<int64_t>(ca->max_blocks) * ca->page_size));
+  p.sinks = j.window > 0 ? j.sinks : 0;
+  p.mh = 0;
+  const int64_t B = j.chunk->batch, T = j.chunk->total_tokens, H = c->num_heads;
+  const int max_new = std::min(j.chunk->max_len, p.max_context);
+  // the longest visible part of a context, in key tiles
+  int64_t seen = p.max_context;
+  if (j.window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(j.window) + max_new + p.sinks);
+  auto tiles_of = [&](int keys) { return static_cast<int>((seen + keys - 1) / keys); };
+  auto groups_of = [&](int rows) { return (max_new + rows - 1) / rows; };
+  // (sequence, head, row group) triples that have rows: at most this many of the grid's
+  auto busy = [&](int rows) { return std::min<int64_t>(B * groups_of(rows), T / rows + B) * H; };
+  if (ca->dtype == HSTU_FP32) {
+    p.kernel = K_PAGED_F32;
+    p.groups = groups_of(PG32_ROWS);
+    p.nsplit = paged_splits(busy(PG32_ROWS), 4 * sm_count, tiles_of(PG32_KEYS));
+  } else {
+    static_assert(PGS_KEYS == PGT_KEYS, "one count of key tiles for both kernels");
+    const int tiles = tiles_of(PGS_KEYS);
+    const int64_t tile_busy = busy(PGT_ROWS);
+    const int tile_ns = paged_splits(tile_busy, sm_count, tiles);
+    p.mh = max_new <= 8 ? 1 : 2;
+    const int64_t rows_busy = busy(8 * p.mh);
+    p.kernel = K_PAGED_ROWS;
+    p.groups = groups_of(8 * p.mh);
+    p.nsplit = paged_splits(rows_busy, 3 * sm_count, tiles);
+    if (max_new > 16 && paged_tile_is_faster(rows_busy, p.nsplit, tile_busy, tile_ns, tiles, max_new,
+                                             c->phi2 == HSTU_ACT_SOFTMAX, sm_count)) {
+      p.kernel = K_PAGED_TILE;
+      p.groups = groups_of(PGT_ROWS);
+      p.nsplit = tile_ns;
+    }
+  }
+  p.ctas = B * p.groups * H;
+  if (p.ctas * p.nsplit > (int64_t(1) << 31) - 1) return HSTU_ERR_UNSUPPORTED;
+  *out = p;
+  return HSTU_OK;
+}
+
 // av: operand type; av_f32 (and ln_part) instead of it when given.
 hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, int layer, const void* q,
                                 int64_t ldq, const float* rab_pos, const float* rab_time, void* av,
@@ -1098,6 +1151,8 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   hstu_status_t s = device_info(&di);
   if (s != HSTU_OK) return s;
   const hstu_cache_t* ca = j.cache;
+  PagedPlan plan;
+  if ((s = plan_paged_attn(c, j, di->sm_count, &plan)) != HSTU_OK) return s;
   PagedParams p;
   std::memset(&p, 0, sizeof(p));
   const size_t layer_bytes =
@@ -1126,10 +1181,11 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   p.max_blocks = ca->max_blocks;
   p.ps_log2 = log2_of(ca->page_size);
   p.max_new = j.chunk->max_len;
-  p.max_context = static_cast<int32_t>(
-      std::min<int64_t>(j.max_context, static_cast<int64_t>(ca->max_blocks) * ca->page_size));
+  p.max_context = plan.max_context;
   p.window = j.window;
-  p.sinks = j.window > 0 ? j.sinks : 0;
+  p.sinks = plan.sinks;
+  p.groups = plan.groups;
+  p.nsplit = plan.nsplit;
   p.timeout_ns = kDefaultTimeoutNs;
   const int64_t* thr = thresholds_for(c->num_time_buckets);
   for (int b = 0; b < c->num_time_buckets; ++b)
@@ -1137,54 +1193,25 @@ hstu_status_t launch_paged_attn(const hstu_layer_cfg_t* c, const PagedJob& j, in
   const int4* oct = octaves_for(c->num_time_buckets);
   if (oct == nullptr) return HSTU_ERR_UNSUPPORTED;
   std::memcpy(p.oct, oct, sizeof(p.oct));
-  const int max_new = std::min(p.max_new, p.max_context);
-  if (max_new == 0) return HSTU_OK;
-  // the longest visible part of a context, in key tiles
-  int64_t seen = p.max_context;
-  if (p.window > 0) seen = std::min<int64_t>(seen, static_cast<int64_t>(p.window) + max_new + p.sinks);
-  auto tiles_of = [&](int keys) { return static_cast<int>((seen + keys - 1) / keys); };
-  // (sequence, head, row group) triples that have rows: at most this many of the grid's
-  auto busy = [&](int rows) {
-    return std::min<int64_t>(static_cast<int64_t>(p.B) * p.groups, p.T / rows + p.B) * p.H;
-  };
-  if (ca->dtype == HSTU_FP32) {
-    p.groups = (max_new + PG32_ROWS - 1) / PG32_ROWS;
-    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-    p.nsplit = paged_splits(busy(PG32_ROWS), 4 * di->sm_count, tiles_of(PG32_KEYS));
+  if (plan.kernel == K_PAGED_F32) {
     ProfScope prof(K_PAGED_F32, st);
-    return launch_cluster(hstu_paged_f32_kernel, ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
+    return launch_cluster(hstu_paged_f32_kernel, plan.ctas, p.nsplit, PG32_THREADS, 0, st, p, c->phi2);
   }
   const bool f16 = ca->dtype == HSTU_FP16;
-  CUtensorMap mkv;
+  CUtensorMap mkv, mq;
   const int64_t map_rows = static_cast<int64_t>(ca->num_pages) * 2 * ca->num_heads * ca->page_size;
   if ((s = make_map_16(&mkv, p.kv, map_rows, 64, 64, 64, std::min(ca->page_size, 64), f16)) != HSTU_OK)
     return s;
-  static_assert(PGS_KEYS == PGT_KEYS, "one count of key tiles for both kernels");
-  const int tiles = tiles_of(PGS_KEYS);
-  const int tile_groups = (max_new + PGT_ROWS - 1) / PGT_ROWS;
-  p.groups = tile_groups;
-  const int64_t tile_busy = busy(PGT_ROWS);
-  const int tile_ns = paged_splits(tile_busy, di->sm_count, tiles);
-  const int mh = max_new <= 8 ? 1 : 2;  // 8-row halves per CTA of the few-rows kernel
-  p.groups = (max_new + 8 * mh - 1) / (8 * mh);
-  const int64_t rows_busy = busy(8 * mh);
-  p.nsplit = paged_splits(rows_busy, 3 * di->sm_count, tiles);
-  if (max_new > 16 && paged_tile_is_faster(rows_busy, p.nsplit, tile_busy, tile_ns, tiles, max_new,
-                                           c->phi2 == HSTU_ACT_SOFTMAX, di->sm_count)) {
-    CUtensorMap mq;
+  if (plan.kernel == K_PAGED_TILE) {
     const int64_t hc = static_cast<int64_t>(p.H) * 64;
     if ((s = make_map_16(&mq, q, p.T, hc, ldq, 64, 128, f16)) != HSTU_OK) return s;
-    p.groups = tile_groups;
-    p.nsplit = tile_ns;
-    const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
     ProfScope prof(K_PAGED_TILE, st);
-    return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), ctas, p.nsplit, PGT_THREADS, PgtSmem::kBytes, st,
-                          mq, mkv, p);
+    return launch_cluster(paged_tile_kernel_ptr(c->phi2, f16), plan.ctas, p.nsplit, PGT_THREADS,
+                          PgtSmem::kBytes, st, mq, mkv, p);
   }
-  const int64_t ctas = static_cast<int64_t>(p.B) * p.groups * p.H;
-  p.sorted = p.B > 1 && p.B <= 128 && ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
+  p.sorted = p.B > 1 && p.B <= 128 && plan.ctas * p.nsplit > 2 * di->sm_count ? 1 : 0;
   ProfScope prof(K_PAGED_ROWS, st);
-  return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, mh), ctas, p.nsplit, PGS_THREADS,
+  return launch_cluster(paged_rows_kernel_ptr(c->phi2, f16, plan.mh), plan.ctas, p.nsplit, PGS_THREADS,
                         PgsSmem::kBytes, st, mkv, p);
 }
 
@@ -2269,6 +2296,10 @@ hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const ReserveWs rws = carve_reserve(cache, chunk->batch, sp + stream_ws_bytes(cfg, T));
   const PagedJob pj{cache, chunk, seq_ids, max_context, window, sinks, rws.state};
+  DeviceInfo* di = nullptr;
+  if ((s = device_info(&di)) != HSTU_OK) return s;
+  PagedPlan plan;
+  if ((s = plan_paged_attn(cfg, pj, di->sm_count, &plan)) != HSTU_OK) return s;
   if ((s = launch_reserve(cache, chunk, seq_ids, &pj, rws, st)) != HSTU_OK) return s;
   AttnJob base;
   std::memset(&base, 0, sizeof(base));

@@ -869,3 +869,25 @@ def test_extend_refuses_what_its_attention_would_report(H):
             assert caches[0].lengths.tolist() == [a + b for a, b in zip(n, cnt)]
         verdicts.append(want)
     assert 6 <= verdicts.count(6) <= 18, verdicts
+
+
+def test_extend_too_large_to_launch(H):
+    """A grid past the launch limit: an error of the call, with no event reserved."""
+    heads, users = 128, 65535
+    dev = dict(device="cuda")
+    cfg = H.LayerConfig(64, heads, 16, 16)
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, **dev)  # noqa: E731
+    f = lambda *s: torch.zeros(*s, dtype=torch.float32, **dev)  # noqa: E731
+    w = [H.LayerWeights(z(4 * heads * 64, 64), f(4 * heads * 64), z(64, heads * 64), f(64), f(heads, 16), f(heads, 16))]
+    cache = H.PagedCache.empty(1, heads, 4, users, 64, 128, "fp16")
+    counts = [0] * users
+    counts[7] = 1
+    j = chunk_of(H, counts, [5])
+    x = z(1, 64)
+    wide = H.Jagged(j.offsets, j.timestamps, 8192, 1)  # up to 8192 events each
+    with pytest.raises(H.HSTUError) as e:
+        H.extend(cfg, w, cache, wide, x, 8192)
+    assert e.value.status == 2 and H.device_status() == 0
+    assert int(cache.lengths.sum()) == 0 and int(cache.ref_count.sum()) == 0 and bool((cache.block_table == -1).all())
+    H.extend(cfg, w, cache, j, x, 8192)
+    assert H.device_status() == 0 and int(cache.lengths[7]) == 1 and int(cache.lengths.sum()) == 1
