@@ -331,42 +331,37 @@ hstu_cache_reserve_rows_kernel(const CacheView c, const int32_t* __restrict__ se
 // ---------------------------------------------------------------- fork, release
 
 // One CTA per fork: the destination (an empty sequence) shares every page of the source.
-__global__ void __launch_bounds__(128)
+// No sequence that is a destination is a source too, and of the forks that name one
+// destination the first is made: every CTA looks through all destinations (256 of them in
+// two loads per thread, which travel with the CTA's own), so that what is made and what
+// is reported does not depend on the order in which CTAs run.
+constexpr int CACHE_FORK_THREADS = 128;
+__global__ void __launch_bounds__(CACHE_FORK_THREADS)
 hstu_cache_fork_kernel(const CacheView c, const int32_t* __restrict__ src_ids,
                        const int32_t* __restrict__ dst_ids) {
-  __shared__ int sN;
   const int src = src_ids[blockIdx.x], dst = dst_ids[blockIdx.x];
-  if (static_cast<uint32_t>(src) >= static_cast<uint32_t>(c.num_seqs) ||
-      static_cast<uint32_t>(dst) >= static_cast<uint32_t>(c.num_seqs)) {
+  bool bad = static_cast<uint32_t>(src) >= static_cast<uint32_t>(c.num_seqs) ||
+             static_cast<uint32_t>(dst) >= static_cast<uint32_t>(c.num_seqs);
+  const int n = bad ? -1 : c.lengths[src];
+  bad = bad || n < 0 || c.blocks(n) > c.max_blocks || c.lengths[dst] != 0;
+#pragma unroll 4
+  for (uint32_t i = threadIdx.x; i < gridDim.x; i += CACHE_FORK_THREADS) {
+    const int d = dst_ids[i];
+    bad |= d == src || (d == dst && i < blockIdx.x);
+  }
+  // (every thread has read the destination's length)
+  if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) record_status(HSTU_ERR_DEVICE_CHECK);
     return;
   }
-  if (threadIdx.x == 0) {
-    // claim the destination: its length leaves 0 once, so a sequence named as a
-    // destination twice is taken by one fork and reported by the other, and one
-    // being forked into is no source (its length is negative meanwhile)
-    int n = *reinterpret_cast<volatile int32_t*>(&c.lengths[src]);
-    if (src == dst || n < 0 || c.blocks(n) > c.max_blocks) {
-      n = -1;
-    } else if (atomicCAS(&c.lengths[dst], 0, n == 0 ? 0 : INT32_MIN) != 0) {
-      n = -1;
-    }
-    if (n < 0) record_status(HSTU_ERR_DEVICE_CHECK);
-    sN = n;
-  }
-  __syncthreads();
-  const int n = sN;
-  if (n <= 0) return;
   const int nb = c.blocks(n);
   const int32_t* a = c.row(src);
   int32_t* b = c.row(dst);
-  for (int i = threadIdx.x; i < nb; i += blockDim.x) {
+  for (int i = threadIdx.x; i < nb; i += CACHE_FORK_THREADS) {
     const int page = a[i];
     b[i] = page;
     if (c.page_ok(page)) atomicAdd(&c.ref[page], 1);
   }
-  __threadfence();
-  __syncthreads();
   if (threadIdx.x == 0) c.lengths[dst] = n;
 }
 

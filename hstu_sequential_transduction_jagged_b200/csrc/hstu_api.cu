@@ -2147,7 +2147,7 @@ hstu_status_t hstu_cache_fork(const hstu_cache_t* cache, int32_t count, const in
   if (count == 0) return HSTU_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(K_CACHE_META, st);
-  hstu_cache_fork_kernel<<<count, 128, 0, st>>>(view_of(cache), src_ids, dst_ids);
+  hstu_cache_fork_kernel<<<count, CACHE_FORK_THREADS, 0, st>>>(view_of(cache), src_ids, dst_ids);
   HSTU_CHECK_CUDA(cudaGetLastError());
   return HSTU_OK;
 }

@@ -434,7 +434,9 @@ hstu_status_t hstu_cache_gather(const hstu_cache_t* cache, int32_t batch, const 
 
 /* Forks count sequences: dst_ids[i] (an empty sequence) becomes a copy of
  * src_ids[i] that shares its pages.  A source may be forked many times in one
- * call; no destination may be named twice or be a source.  device int32 [count]. */
+ * call; no destination may be named twice or be a source: a fork from a sequence that is a
+ * destination, or into one that an earlier fork of the call names, is reported and not
+ * made, and the others are.  device int32 [count]. */
 hstu_status_t hstu_cache_fork(const hstu_cache_t* cache, int32_t count, const int32_t* src_ids,
                               const int32_t* dst_ids, void* stream);
 

@@ -891,3 +891,43 @@ def test_extend_too_large_to_launch(H):
     assert int(cache.lengths.sum()) == 0 and int(cache.ref_count.sum()) == 0 and bool((cache.block_table == -1).all())
     H.extend(cfg, w, cache, j, x, 8192)
     assert H.device_status() == 0 and int(cache.lengths[7]) == 1 and int(cache.lengths.sum()) == 1
+
+
+@pytest.mark.parametrize("count", [2, 40, 1000])
+def test_fork_does_not_depend_on_the_order_of_blocks(H, count):
+    """Sources that are destinations too, and destinations named twice, in one call: the same
+    forks are made and reported every time."""
+    def fresh():
+        cache = nan_cache(H, layers=1, heads=1, pages=40, seqs=count + 4, blocks=4, ps=16, dtype="fp16")
+        H.cache_reserve(cache, chunk_of(H, [20], range(20)), seq_ids=i32([0]))
+        return cache
+
+    def after(cache, src, dst):
+        H.cache_fork(cache, i32(src), i32(dst))
+        return H.device_status()
+
+    for _ in range(5):
+        # a chain 0 -> 1 -> 2 ..: only the first is from no destination
+        cache = fresh()
+        assert after(cache, range(count), range(1, count + 1)) == 6
+        assert cache.lengths.tolist() == [20, 20] + [0] * (count + 2)
+        assert cache.ref_count.tolist()[:2] == [2, 2] and int((cache.block_table >= 0).sum()) == 4
+        # a ring of empty sequences
+        assert after(cache, [3, 2], [2, 3]) == 6
+        # two sources, one of them empty, for one destination: the first is made
+        for src, want in (([0, 3], 20), ([3, 0], 0)):
+            cache = fresh()
+            assert after(cache, src, [1, 1]) == 6
+            assert cache.lengths.tolist() == [20, want] + [0] * (count + 2)
+            assert cache.ref_count.tolist()[:2] == [1 + (want > 0)] * 2
+        cache = fresh()
+        assert after(cache, [2, 3], [1, 1]) == 6   # two empty sources
+        # and what is allowed: one source, every other sequence, empty sources too
+        cache = fresh()
+        assert after(cache, [0] * (count + 2), range(1, count + 3)) == 0
+        assert cache.lengths.tolist() == [20] * (count + 3) + [0]
+        assert cache.ref_count.tolist()[:2] == [count + 3] * 2
+        assert after(cache, [count + 3], [count + 3]) == 6
+        H.cache_release(cache, i32([1, 2]))
+        assert after(cache, [1], [2]) == 0
+        assert after(cache, [1], [0]) == 6          # an empty source, a destination that is not
