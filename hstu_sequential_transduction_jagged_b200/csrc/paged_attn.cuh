@@ -271,11 +271,13 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
       for (int d = 8; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       const float2 old = sm.ml[r];
       m = fmaxf(m, old.x);
+      // (the maximum passes a NaN over: it stays one in its weight and in the sum)
       const bool any = m > -INFINITY;
-      y.x = any ? expf(y.x - m) : 0.0f;
-      y.y = any ? expf(y.y - m) : 0.0f;
-      y.z = any ? expf(y.z - m) : 0.0f;
-      y.w = any ? expf(y.w - m) : 0.0f;
+      const float mm = any ? m : 0.0f;
+      y.x = expf(y.x - mm);
+      y.y = expf(y.y - mm);
+      y.z = expf(y.z - mm);
+      y.w = expf(y.w - mm);
       *reinterpret_cast<float4*>(&sm.s[r][4 * c4]) = y;
       float l = (y.x + y.y) + (y.z + y.w);
 #pragma unroll
@@ -320,7 +322,7 @@ hstu_paged_f32_kernel(const __grid_constant__ PagedParams p, int phi2) {
         l += o_sm->ml[r].y * f;
         o += o_sm->v[r][col] * f;
       }
-      o = l > 0.0f ? o / l : 0.0f;
+      o = l == 0.0f ? 0.0f : o / l;  // a NaN stays one
     } else {
       for (int k = 0; k < p.nsplit; ++k) o += cluster.map_shared_rank(&sm, k)->v[r][col];
       o /= static_cast<float>(n_all);

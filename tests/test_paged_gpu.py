@@ -931,3 +931,42 @@ def test_fork_does_not_depend_on_the_order_of_blocks(H, count):
         H.cache_release(cache, i32([1, 2]))
         assert after(cache, [1], [2]) == 0
         assert after(cache, [1], [0]) == 6          # an empty source, a destination that is not
+
+
+@pytest.mark.parametrize("dtype,heads,lens,kernel", [
+    ("fp32", 2, [(40, 3), (700, 20)], "fp32"), ("fp16", 2, [(40, 3), (700, 16)], "rows"),
+    ("bf16", 8, [(300, 120), (700, 128)] * 6, "rows"), ("bf16", 8, [(300, 120), (700, 128)] * 20, "tile")])
+def test_softmax_keeps_nan(H, dtype, heads, lens, kernel):
+    """A row of Q with a NaN, and a key with a NaN: the rows that see them are NaN in that head,
+    and the others are what they are without."""
+    counts = [c for _, c in lens]
+    ac = make_attn_case([n for n, _ in lens], heads, 64, 64, seed=31, dtype=dtype)
+    cache = nan_cache(H, layers=1, heads=heads, pages=sum(-(-n // 16) for n, _ in lens) + 4, seqs=len(lens), blocks=50,
+                      ps=16, dtype=dtype)
+    j, rows = load_cache(H, ac, cache, counts)
+    cfg = H.LayerConfig(64 * heads, heads, 64, 64, phi2="softmax", dtype=dtype)
+    q = tensor(ac.q[rows], DT[dtype], "cuda")
+    rp, rt = tensor(ac.rab_pos, torch.float32, "cuda"), tensor(ac.rab_time, torch.float32, "cuda")
+    ctx = max(n for n, _ in lens)
+    H.profiler_start()
+    clean = H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, ctx)
+    assert set(H.profiler_stop()) == {"paged_attention_" + kernel}
+    q2 = q.clone()
+    q2[1, 64 + 5] = float("nan")
+    got = H.paged_attn_fwd(cfg, cache, 0, j, q2, rp, rt, ctx)
+    assert bool(got[1, 64:128].isnan().all())
+    got[1, 64:128] = clean[1, 64:128]
+    assert torch.equal(got, clean)
+    # a key of the second sequence: event 0, seen by all its rows, and the last one, by itself
+    n, c = lens[1]
+    r0 = counts[0]
+    for at, seen in ((0, slice(r0, r0 + c)), (n - 1, slice(r0 + c - 1, r0 + c))):
+        page = int(cache.block_table[1, at // 16])
+        old = float(cache.kv[0, page, 0, 0, at % 16, 3])
+        cache.kv[0, page, 0, 0, at % 16, 3] = float("nan")
+        got = H.paged_attn_fwd(cfg, cache, 0, j, q, rp, rt, ctx)
+        cache.kv[0, page, 0, 0, at % 16, 3] = old
+        assert bool(got[seen, :64].isnan().all())
+        got[seen, :64] = clean[seen, :64]
+        assert torch.equal(got, clean)
+    assert H.device_status() == 0
