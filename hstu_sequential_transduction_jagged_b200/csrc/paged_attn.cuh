@@ -17,7 +17,7 @@
 // rab_pos (i - j runs over keys + rows - 1 values), loaded per tile, so neither
 // the sequence length nor the table has to fit shared memory.  Times are int32
 // seconds relative to the last event (offset so that they stay non-negative); a
-// visible key 2^31 - 3 seconds or more before it is reported.
+// visible key more than 2^31 - 3 seconds before it is reported.
 #pragma once
 
 #include <cooperative_groups.h>

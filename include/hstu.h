@@ -469,7 +469,7 @@ hstu_status_t hstu_cache_compact(const hstu_cache_t* cache, int32_t* live_out, v
  * Any sequence length that the block table holds.  Values of V that some row of the chunk
  * sees must be finite (a product with a masked weight is still formed);
  * everything else, unwritten slots of a page included, may hold anything.  A
- * visible event 2^31 - 3 seconds or more before the last one is reported.  One launch;
+ * visible event more than 2^31 - 3 seconds before the last one is reported.  One launch;
  * needs no workspace; bit-reproducible. */
 hstu_status_t hstu_paged_attn_fwd(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
                                   int32_t layer, const hstu_jagged_t* chunk,

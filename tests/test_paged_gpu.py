@@ -970,3 +970,24 @@ def test_softmax_keeps_nan(H, dtype, heads, lens, kernel):
         got[seen, :64] = clean[seen, :64]
         assert torch.equal(got, clean)
     assert H.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,c", [("fp16", 3), ("fp16", 200), ("bf16", 3), ("bf16", 200), ("fp32", 3), ("fp32", 200)])
+def test_the_longest_span(H, dtype, c):
+    """An event 2^31 - 3 seconds before the last one is taken as it is, one second more is reported."""
+    ac = make_attn_case([250], 1, 16, 128, seed=2, dtype=dtype)
+    for span, want_status in ((2 ** 31 - 3, 0), (2 ** 31 - 2, 6)):
+        ac.timestamps[:] = 1_700_000_000 + span
+        ac.timestamps[0] = 1_700_000_000
+        cache = nan_cache(H, layers=1, heads=1, pages=20, seqs=1, blocks=16, ps=16, dtype=dtype)
+        j, rows = load_cache(H, ac, cache, [c])
+        cfg = H.LayerConfig(64, 1, 16, 128, dtype=dtype)
+        got = H.paged_attn_fwd(cfg, cache, 0, j, tensor(ac.q[rows], DT[dtype], "cuda"),
+                               tensor(ac.rab_pos, torch.float32, "cuda"),
+                               tensor(ac.rab_time, torch.float32, "cuda"), 250)
+        assert H.device_status() == want_status, span
+        if want_status == 0:
+            f = np.float64
+            want = P.chunk_attention(ac.q[250 - c:].astype(f), ac.k.astype(f), ac.v.astype(f), ac.timestamps,
+                                     ac.rab_pos.astype(f), ac.rab_time.astype(f), 1)
+            assert_close(got.float().cpu().numpy(), want, f"span {span} {dtype}", scaled=True)
