@@ -968,7 +968,7 @@ size_t cache_ws_bytes(const hstu_cache_t* c, int32_t batch) {
   return 256 + std::max(b + pages, 3 * pages);
 }
 
-ReserveWs carve_reserve(const hstu_cache_t*, int32_t batch, void* ws) {
+ReserveWs carve_reserve(int32_t batch, void* ws) {
   ReserveWs r;
   uint8_t* p = static_cast<uint8_t*>(ws);
   r.state = reinterpret_cast<int32_t*>(p);
@@ -2095,7 +2095,7 @@ hstu_status_t hstu_cache_reserve(const hstu_cache_t* cache, const hstu_jagged_t*
   if (!aligned16(workspace)) return HSTU_ERR_INVALID_ARGUMENT;
   if (workspace == nullptr || ws_bytes < cache_ws_bytes(cache, chunk->batch))
     return HSTU_ERR_WORKSPACE_TOO_SMALL;
-  return launch_reserve(cache, chunk, seq_ids, nullptr, carve_reserve(cache, chunk->batch, workspace),
+  return launch_reserve(cache, chunk, seq_ids, nullptr, carve_reserve(chunk->batch, workspace),
                         static_cast<cudaStream_t>(stream));
 }
 
@@ -2294,7 +2294,7 @@ hstu_status_t hstu_extend(const hstu_layer_cfg_t* cfg, int32_t num_layers,
   float* yf[2] = {reinterpret_cast<float*>(sp), reinterpret_cast<float*>(sp + fbytes)};
   void* yl[2] = {sp + 2 * fbytes, sp + 2 * fbytes + lbytes};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const ReserveWs rws = carve_reserve(cache, chunk->batch, sp + stream_ws_bytes(cfg, T));
+  const ReserveWs rws = carve_reserve(chunk->batch, sp + stream_ws_bytes(cfg, T));
   const PagedJob pj{cache, chunk, seq_ids, max_context, window, sinks, rws.state};
   DeviceInfo* di = nullptr;
   if ((s = device_info(&di)) != HSTU_OK) return s;

@@ -53,9 +53,6 @@ struct PagedParams {
   int4 oct[32];
 };
 
-
-__device__ __forceinline__ int log2_small(int v) { return 31 - __clz(v); }
-
 // One sequence's part of a launch, the same for every CTA of its clusters; tiles of
 // KEYS keys.
 template <int KEYS>

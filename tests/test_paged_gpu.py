@@ -991,3 +991,44 @@ def test_the_longest_span(H, dtype, c):
             want = P.chunk_attention(ac.q[250 - c:].astype(f), ac.k.astype(f), ac.v.astype(f), ac.timestamps,
                                      ac.rab_pos.astype(f), ac.rab_time.astype(f), 1)
             assert_close(got.float().cpu().numpy(), want, f"span {span} {dtype}", scaled=True)
+
+
+@pytest.mark.parametrize("ps", [16, 64])
+def test_whole_rows_of_the_block_table(H, ps):
+    """Every entry of every block-table row after each call, those past the length included: a
+    released block is -1, and so is one that was never given out."""
+    rng = np.random.default_rng(100 + ps)
+    seqs, blocks, pages = 6, 7, 24
+    cache = nan_cache(H, layers=1, heads=1, pages=pages, seqs=seqs, blocks=blocks, ps=ps, dtype="fp16")
+    pg = P.Pages(pages, seqs, blocks, ps)
+    done = {op: 0 for op in ("reserve", "refused", "fork", "release", "trim", "compact")}
+    for _ in range(150):
+        op = str(rng.choice(["reserve", "reserve", "fork", "release", "trim", "compact"]))
+        if op == "reserve":
+            ids = rng.permutation(seqs)[:int(rng.integers(1, 4))].tolist()
+            cnt = [int(v) for v in rng.integers(0, 3 * ps, len(ids))]
+            ok = pg.reserve(ids, cnt) is not None
+            op = op if ok else "refused"
+            H.cache_reserve(cache, chunk_of(H, cnt, range(sum(cnt))), seq_ids=i32(ids))
+            assert H.device_status() == (0 if ok else 6)
+        elif op == "fork":
+            full, empty = [s for s in range(seqs) if pg.len[s]], [s for s in range(seqs) if not pg.len[s]]
+            if not full or not empty:
+                continue
+            H.cache_fork(cache, i32(full[:1]), i32(empty[:1]))
+            pg.fork(full[0], empty[0])
+        elif op == "release":
+            s = int(rng.integers(seqs))
+            H.cache_release(cache, i32([s]))
+            pg.release(s)
+        elif op == "trim":
+            s, w, k = int(rng.integers(seqs)), int(rng.integers(1, 3 * ps)), int(rng.integers(0, 2 * ps))
+            H.cache_release(cache, i32([s]), window=w, sinks=k)
+            pg.release(s, w, k)
+        else:
+            H.cache_compact(cache)
+            pg.compact()
+        done[op] += 1
+        assert H.device_status() == 0
+        assert tables(cache) == (pg.table, pg.len, pg.ref)
+    assert min(done.values()) > 0, done
