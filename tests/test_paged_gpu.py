@@ -1032,3 +1032,41 @@ def test_whole_rows_of_the_block_table(H, ps):
         assert H.device_status() == 0
         assert tables(cache) == (pg.table, pg.len, pg.ref)
     assert min(done.values()) > 0, done
+
+
+@pytest.mark.parametrize("users", [128, 129, 300])
+@pytest.mark.parametrize("phi2", ["silu", "softmax"])
+def test_attention_of_many_users(H, phi2, users):
+    """The few-rows kernel with and without its order by length (up to 128 sequences): ragged users,
+    some of them without events or without new ones."""
+    rng = np.random.default_rng(users)
+    n = [int(v) for v in rng.integers(0, 400, users)]
+    run_attn(H, [(v, min(v, int(rng.integers(0, 6)))) for v in n], 4, "fp16", phi2, 32, kernel="rows")
+
+
+@pytest.mark.parametrize("phi2", ["silu", "softmax"])
+@pytest.mark.parametrize("window,sinks", [(40, 9), (1, 0), (16, 50)])
+def test_extend_fp32_through_a_window(H, phi2, window, sinks):
+    """A stack of fp32 layers through a window with sinks, in several requests, its pages released behind it."""
+    case = make_case(make_case("tiny-fp32").cfg.replace(phi2=phi2, num_layers=2), seed=33, lengths=[130, 64, 1, 47])
+    cfg = config_of(H, case.cfg)
+    t = case_tensors(case, "cuda")
+    weights = [H.LayerWeights(**lw) for lw in t["layers"]]
+    cache = nan_cache(H, layers=2, heads=case.cfg.num_heads, pages=40, seqs=4, blocks=9, ps=16, dtype="fp32")
+    cuts = [[0, 100, 101, 130], [0, 10, 63, 64], [0, 0, 1, 1], [0, 30, 30, 47]]
+    state = [None] * 4
+    for step in range(3):
+        rows = np.concatenate([case.offsets[u] + np.arange(cuts[u][step], cuts[u][step + 1]) for u in range(4)])
+        j = chunk_of(H, [cuts[u][step + 1] - cuts[u][step] for u in range(4)], case.timestamps[rows])
+        y = H.extend(cfg, weights, cache, j, t["x"][torch.from_numpy(rows).cuda()].contiguous(), 130, window=window,
+                     sinks=sinks)
+        H.cache_release(cache, i32(range(4)), window=window, sinks=sinks)
+        assert H.device_status() == 0
+        want = []
+        for u in range(4):
+            a, b = case.offsets[u] + cuts[u][step], case.offsets[u] + cuts[u][step + 1]
+            if b > a:
+                w, state[u] = P.extend(state[u], case.x[a:b], case.timestamps[a:b], case.layers, case.cfg,
+                                       window=window, sinks=sinks)
+                want.append(w)
+        assert_close(y.cpu().numpy(), np.concatenate(want), f"extend fp32 {phi2} {window} {sinks} step {step}")
