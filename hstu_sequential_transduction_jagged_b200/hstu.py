@@ -515,6 +515,14 @@ class PagedCache(namedtuple("PagedCache", "kv timestamps ref_count block_table l
             torch.zeros(num_pages, **i32), torch.full((num_seqs, max_blocks), -1, **i32),
             torch.zeros(num_seqs, **i32))
 
+    def _replace(self, **kw):
+        """A handle with other tensors in some places (a tuple's own would keep the old
+        addresses)."""
+        parts = [kw.pop(name, old) for name, old in zip(self._fields[:5], self)]
+        if kw:
+            raise ValueError(f"PagedCache: no tensor named {sorted(kw)}")
+        return PagedCache(*parts)
+
     def c(self) -> CacheT:
         return self.desc
 

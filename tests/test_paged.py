@@ -310,3 +310,17 @@ def test_binding_refuses_what_pointers_would_misread(H):
               lambda: H.cache_release(cache, ids), lambda: H.cache_compact(cache), attn, ext,
               lambda: attn(H.paged_attn_fwd_f32)):
         refused("not on the current GPU", f)
+
+
+def test_a_replaced_part_is_described_anew(H):
+    import torch
+    i32 = torch.int32
+    cache = H.PagedCache(torch.zeros(1, 4, 2, 1, 16, 64), torch.zeros(4, 16, dtype=torch.int64), torch.zeros(4, dtype=i32),
+                         torch.zeros(3, 5, dtype=i32), torch.zeros(3, dtype=i32))
+    other = torch.zeros(3, dtype=i32)
+    got = cache._replace(lengths=other)
+    assert got.lengths is other and got.c().lengths == other.data_ptr() and got.c().kv == cache.kv.data_ptr()
+    assert cache.c().lengths == cache.lengths.data_ptr()
+    for kw in (dict(lengths=torch.zeros(4, dtype=i32)), dict(desc=cache.desc), dict(size=3)):
+        with pytest.raises(ValueError):
+            cache._replace(**kw)
