@@ -2144,10 +2144,19 @@ hstu_status_t hstu_cache_fork(const hstu_cache_t* cache, int32_t count, const in
   if ((s = check_cache(cache, true)) != HSTU_OK) return s;
   if (count < 0 || (count > 0 && (src_ids == nullptr || dst_ids == nullptr)))
     return HSTU_ERR_INVALID_ARGUMENT;
+  if (count >= (1 << 30)) return HSTU_ERR_UNSUPPORTED;
   if (count == 0) return HSTU_OK;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ProfScope prof(K_CACHE_META, st);
-  hstu_cache_fork_kernel<<<count, CACHE_FORK_THREADS, 0, st>>>(view_of(cache), src_ids, dst_ids);
+  const CacheView v = view_of(cache);
+  if (count <= CACHE_FORK_SCAN) {
+    hstu_cache_fork_kernel<false><<<count, CACHE_FORK_THREADS, 0, st>>>(v, src_ids, dst_ids);
+  } else {
+    const unsigned blocks = (static_cast<unsigned>(count) + CACHE_COPY_THREADS - 1) / CACHE_COPY_THREADS;
+    hstu_cache_fork_mark_kernel<<<blocks, CACHE_COPY_THREADS, 0, st>>>(v, count, dst_ids);
+    hstu_cache_fork_kernel<true><<<count, CACHE_FORK_THREADS, 0, st>>>(v, src_ids, dst_ids);
+    hstu_cache_fork_clear_kernel<<<blocks, CACHE_COPY_THREADS, 0, st>>>(v, count, dst_ids);
+  }
   HSTU_CHECK_CUDA(cudaGetLastError());
   return HSTU_OK;
 }

@@ -324,3 +324,7 @@ def test_a_replaced_part_is_described_anew(H):
     for kw in (dict(lengths=torch.zeros(4, dtype=i32)), dict(desc=cache.desc), dict(size=3)):
         with pytest.raises(ValueError):
             cache._replace(**kw)
+
+
+def test_more_forks_than_indexes_are_refused(H):
+    assert H.lib().hstu_cache_fork(ctypes.byref(_cache(H)), 1 << 30, 4096, 4096, None) == 2

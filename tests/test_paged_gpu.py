@@ -1070,3 +1070,58 @@ def test_extend_fp32_through_a_window(H, phi2, window, sinks):
                                        window=window, sinks=sinks)
                 want.append(w)
         assert_close(y.cpu().numpy(), np.concatenate(want), f"extend fp32 {phi2} {window} {sinks} step {step}")
+
+
+@pytest.mark.parametrize("count", [3, 500, 4096, 4097, 9000])
+def test_forks_follow_the_rule(H, count):
+    """Random forks, most of them allowed: those from a sequence that is a destination, into one
+    that an earlier fork names or that is not empty, and out of range ones are left out, below
+    and above the number from which the destinations are marked."""
+    rng = np.random.default_rng(count)
+    seqs = 2 * count + 20
+    pages = seqs // 2 + 60
+    cache = nan_cache(H, layers=1, heads=1, pages=pages, seqs=seqs, blocks=3, ps=16, dtype="fp16")
+    full = rng.permutation(seqs)[:min(20, seqs // 3)].tolist()
+    kept = set(full)
+    n = [int(v) for v in rng.integers(1, 49, len(full))]
+    H.cache_reserve(cache, chunk_of(H, n, range(sum(n))), seq_ids=i32(full))
+    assert H.device_status() == 0
+    for trial in range(6):
+        lens, ref, table = cache.lengths.tolist(), cache.ref_count.tolist(), cache.block_table.tolist()
+        empty = [s for s in range(seqs) if lens[s] == 0]
+        dst = rng.permutation(empty)[:count].tolist()
+        dst += rng.permutation(seqs)[:count - len(dst)].tolist()
+        to = set(dst)
+        pool = [s for s in full if lens[s]] + [s for s in empty if s not in to][:3]
+        src = [int(v) for v in rng.choice(pool, count)]
+        if trial % 2:
+            for _ in range(max(1, count // 50)):
+                i, k = (int(v) for v in rng.integers(0, count, 2))
+                what = int(rng.integers(5))
+                if what == 0:
+                    dst[i] = dst[k]
+                elif what == 1:
+                    src[i] = dst[k]
+                elif what == 2:
+                    dst[i] = full[0]
+                elif what == 3:
+                    src[i] = int(rng.choice([-1, seqs, 2 ** 31 - 1, -2 ** 31]))
+                else:
+                    dst[i] = int(rng.choice([-1, seqs]))
+        named, taken, bad = set(dst), set(), 0
+        for s, d in zip(src, dst):
+            ok = 0 <= s < seqs and 0 <= d < seqs and s not in named and d not in taken and table[d][0] < 0 and lens[d] == 0
+            taken.add(d)
+            if ok and lens[s]:
+                blocks = -(-lens[s] // 16)
+                for b in range(blocks):
+                    table[d][b] = table[s][b]
+                    ref[table[s][b]] += 1
+                lens[d] = lens[s]
+            bad += not ok
+        H.cache_fork(cache, i32(src), i32(dst))
+        assert H.device_status() == (6 if bad else 0), (trial, bad)
+        assert cache.lengths.tolist() == lens and cache.ref_count.tolist() == ref
+        assert cache.block_table.tolist() == table
+        H.cache_release(cache, i32([s for s in range(seqs) if lens[s] and s not in kept] or full[:1]))
+        assert H.device_status() == 0
