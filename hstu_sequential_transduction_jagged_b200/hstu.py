@@ -638,7 +638,8 @@ def cache_fork(cache: PagedCache, src_ids, dst_ids, stream=None):
 
 
 def cache_release(cache: PagedCache, seq_ids, window: int = 0, sinks: int = 0, stream=None):
-    """Release whole sequences, or with a window the pages that no later event sees."""
+    """Release whole sequences, or with a window the pages that no later event sees
+    through it (later extensions take no wider one)."""
     n = seq_ids.numel()
     ids = _ids(seq_ids, n, "cache_release")
     raw = _cache_stream(cache, stream, "cache_release", seq_ids)

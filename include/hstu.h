@@ -376,13 +376,17 @@ hstu_status_t mfalcon_score(const hstu_layer_cfg_t* cfg, int32_t num_layers,
  * ranges of each sequence's new events (chunk->total_tokens rows in all, at most
  * chunk->max_len per sequence, 0 allowed), chunk->timestamps their times;
  * seq_ids device int32 [batch] names the sequences (NULL: 0 .. batch-1), each at
- * most once.  After hstu_cache_reserve the chunk's rows are the last events of
- * their sequences, and that is where append and attention find them.
+ * most once (a reservation that names one twice is refused; append alone would write
+ * both into the same slots, in no order).  After hstu_cache_reserve the chunk's rows are
+ * the last events of their sequences, and that is where append and attention find them.
  *
- * What the device finds wrong (a sequence out of range or named twice, a block
- * table or pool that is too small, a page that is missing where a row sees it, a
- * shared page that append would write) is reported as HSTU_ERR_DEVICE_CHECK in
- * the device status word; nothing is read or written out of range.
+ * What the device finds wrong (a sequence out of range, a block table or pool that is
+ * too small, a page that is missing where a row sees it, a shared page that append would
+ * write, and what the calls name below) is reported as HSTU_ERR_DEVICE_CHECK in the
+ * device status word; nothing is read or written out of range.
+ *
+ * A workspace belongs to one call until that call has run: calls that may run at once
+ * (on two streams, in two graphs) take one each.
  */
 typedef struct {
   int32_t num_layers;
@@ -470,7 +474,9 @@ hstu_status_t hstu_cache_compact(const hstu_cache_t* cache, int32_t* live_out, v
  * sees must be finite (a product with a masked weight is still formed);
  * everything else, unwritten slots of a page included, may hold anything.  A
  * visible event more than 2^31 - 3 seconds before the last one is reported.  One launch;
- * needs no workspace; bit-reproducible. */
+ * needs no workspace.  Equal calls give equal bits; which kernel runs and in how many parts
+ * it adds up the keys goes by the sizes of the whole batch, so a sequence's last bits may
+ * differ in other company. */
 hstu_status_t hstu_paged_attn_fwd(const hstu_layer_cfg_t* cfg, const hstu_cache_t* cache,
                                   int32_t layer, const hstu_jagged_t* chunk,
                                   const int32_t* seq_ids, int32_t max_context, int32_t window,
