@@ -552,16 +552,16 @@ def _cache_stream(cache: PagedCache, stream, what: str, *tensors) -> int:
     return stream.cuda_stream
 
 
-def _chunk(chunk: Jagged, what: str) -> JaggedT:
-    """The chunk's C description."""
-    o, t, i64 = chunk.offsets, chunk.timestamps, torch.int64
-    total, rows, seg = chunk.total_tokens, t.numel(), chunk.segments
-    if not (o.dtype is i64 and t.dtype is i64 and rows >= total and o.is_contiguous()
-            and t.is_contiguous()):
+def _chunk(chunk: Jagged, what: str):
+    """The chunk's C description and its timestamps (None: it has no rows, and needs none)."""
+    o, i64, total, seg = chunk.offsets, torch.int64, chunk.total_tokens, chunk.segments
+    t = chunk.timestamps if total else None
+    if not (o.dtype is i64 and o.is_contiguous()
+            and (t is None or (t.dtype is i64 and t.numel() >= total and t.is_contiguous()))):
         raise ValueError(f"{what}: the chunk needs contiguous int64 offsets and int64 timestamps "
                          "of total_tokens rows")
-    return JaggedT(o.numel() - 1, total, chunk.max_len, o.data_ptr(), t.data_ptr() if rows else None,
-                   None if seg is None else seg.data_ptr(), chunk.max_static)
+    return JaggedT(o.numel() - 1, total, chunk.max_len, o.data_ptr(), None if t is None else t.data_ptr(),
+                   None if seg is None else seg.data_ptr(), chunk.max_static), t
 
 
 def _dense(t: torch.Tensor, shape, dtype, what: str, name: str):
@@ -579,9 +579,9 @@ def cache_reserve(cache: PagedCache, chunk: Jagged, seq_ids=None, workspace=None
     sequence) and lengthen the sequences; shared partial last pages are copied.
     A pool that is too small leaves everything as it was and is reported in
     device_status()."""
-    c, j = cache.c(), _chunk(chunk, "cache_reserve")
+    c, (j, times) = cache.c(), _chunk(chunk, "cache_reserve")
     ids = _ids(seq_ids, j.batch, "cache_reserve")
-    raw = _cache_stream(cache, stream, "cache_reserve", chunk.offsets, chunk.timestamps, seq_ids, workspace)
+    raw = _cache_stream(cache, stream, "cache_reserve", chunk.offsets, times, seq_ids, workspace)
     if workspace is None:
         nbytes = lib().hstu_cache_workspace_bytes(ctypes.byref(c), j.batch)
         workspace = _workspace(nbytes, cache.kv.device, None, stream)
@@ -602,9 +602,9 @@ def cache_append(cache: PagedCache, layer: int, chunk: Jagged, k, v, seq_ids=Non
     dtype, rows = cache.kv.dtype, (chunk.total_tokens, cache.desc.num_heads * 64)
     if k.dtype is not dtype or v.dtype is not dtype or k.shape != rows or v.shape != rows:
         raise ValueError("cache_append: k and v must be [total_tokens, num_heads * 64] in the cache's type")
-    c, j = cache.c(), _chunk(chunk, "cache_append")
+    c, (j, times) = cache.c(), _chunk(chunk, "cache_append")
     ids = _ids(seq_ids, j.batch, "cache_append")
-    raw = _cache_stream(cache, stream, "cache_append", k, v, chunk.offsets, chunk.timestamps, seq_ids)
+    raw = _cache_stream(cache, stream, "cache_append", k, v, chunk.offsets, times, seq_ids)
     _check(lib().hstu_cache_append(ctypes.byref(c), layer, ctypes.byref(j), ids, k.data_ptr(),
                                    _rows_ld(k, "k"), v.data_ptr(), _rows_ld(v, "v"), raw),
            "hstu_cache_append")
@@ -671,9 +671,9 @@ def _paged_attn(fn, cfg, cache, layer, chunk, q, rab_pos, rab_time, max_context,
     _dense(rab_time, (heads, cfg.num_time_buckets), f32, fn, "rab_time")
     if av_out is not None:
         _dense(av_out, rows, out_dtype, fn, "av_out")
-    c, j = cfg.c(), _chunk(chunk, fn)
+    c, (j, times) = cfg.c(), _chunk(chunk, fn)
     ids = None if seq_ids is None else _ids(seq_ids, j.batch, fn)
-    raw = _cache_stream(cache, stream, fn, q, rab_pos, rab_time, chunk.offsets, chunk.timestamps,
+    raw = _cache_stream(cache, stream, fn, q, rab_pos, rab_time, chunk.offsets, times,
                         seq_ids, av_out)
     if av_out is None:
         if stream is None and out_dtype is q.dtype:  # less host work than a shape and a device
@@ -724,9 +724,9 @@ def extend(cfg: LayerConfig, weights: Sequence[LayerWeights], cache: PagedCache,
     _dense(x_in, rows, cfg.torch_dtype, "extend", "x_in")
     if y_out is not None:
         _dense(y_out, rows, torch.float32, "extend", "y_out")
-    c, ca, j = cfg.c(), cache.c(), _chunk(chunk, "extend")
+    c, ca, (j, times) = cfg.c(), cache.c(), _chunk(chunk, "extend")
     ids = _ids(seq_ids, j.batch, "extend")
-    raw = _cache_stream(cache, stream, "extend", x_in, chunk.offsets, chunk.timestamps, seq_ids,
+    raw = _cache_stream(cache, stream, "extend", x_in, chunk.offsets, times, seq_ids,
                         y_out, workspace)
     if y_out is None:
         y_out = _empty(rows, torch.float32, dev, stream)

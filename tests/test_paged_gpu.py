@@ -1125,3 +1125,26 @@ def test_forks_follow_the_rule(H, count):
         assert cache.block_table.tolist() == table
         H.cache_release(cache, i32([s for s in range(seqs) if lens[s] and s not in kept] or full[:1]))
         assert H.device_status() == 0
+
+
+def test_chunks_without_rows(H):
+    """No new events at all: nothing is needed of the timestamps, and nothing happens."""
+    case = make_case("small-bf16", seed=41, lengths=[20])
+    cfg = config_of(H, case.cfg)
+    weights = [H.LayerWeights(**lw) for lw in case_tensors(case, "cuda")["layers"]]
+    heads = case.cfg.num_heads
+    cache = nan_cache(H, layers=case.cfg.num_layers, heads=heads, pages=6, seqs=2, blocks=4, ps=16, dtype="fp16")
+    H.cache_reserve(cache, chunk_of(H, [20, 0], range(20)))
+    before = tables(cache)
+    rows = torch.empty((0, heads * 64), dtype=torch.float16, device="cuda")
+    rp = torch.zeros((heads, 16), device="cuda")
+    for offsets in (i32([0, 0, 0]).long(), i32([0]).long()):
+        for times in (torch.empty(0), torch.empty(0, dtype=torch.int64, device="cuda"), torch.arange(5)):
+            j = H.Jagged(offsets, times, 0, 0)
+            H.cache_reserve(cache, j)
+            H.cache_append(cache, 0, j, rows, rows)
+            acfg = H.LayerConfig(heads * 64, heads, 16, 16, dtype="fp16")
+            assert H.paged_attn_fwd(acfg, cache, 0, j, rows, rp, rp, 20).shape == rows.shape
+            y = H.extend(cfg, weights, cache, j, torch.empty((0, case.cfg.d_model), dtype=torch.bfloat16, device="cuda"), 20)
+            assert y.shape == (0, case.cfg.d_model)
+    assert H.device_status() == 0 and tables(cache) == before
